@@ -490,6 +490,176 @@ int mk_decode_step_static(const mk_config *cfg, const mk_packed_weights *w, cons
                           float *logits_out, int32_t *next_tok_out, int32_t *status_out,
                           mk_stream_t stream);
 
+/* ---- serving operators ---------------------------------------------- */
+
+/*
+ * Operators of a serving loop around the decode step, without a context:
+ * appending rotated keys and values to a paged cache, attention of one new
+ * token per sequence over such a cache, causal attention over packed
+ * prompts, and sampling the next token from a row of logits.  The pages
+ * describing the decode step have no counterpart of paging, packing or
+ * sampling; they are additions of this library next to the step's own
+ * attention, append and argmax.
+ *
+ * Conventions, besides those at the top of this header:
+ *  - Every call enqueues on `stream` and returns; nothing is allocated,
+ *    nothing is kept between calls, and calls on different streams are
+ *    independent as long as their outputs and workspaces are.  All of them
+ *    may be captured into CUDA graphs.
+ *  - Strides count elements between consecutive tokens (rows); the heads of a
+ *    token and the elements of a head are contiguous.  16-bit buffers are
+ *    16-byte aligned and their strides are multiples of 8 elements and at
+ *    least the row they hold; anything else is MK_ERR_INVALID.
+ *  - status_out: device int32 [1] or NULL.  A call that meets a bad value in
+ *    device memory (see each operator) writes MK_ERR_INVALID there in
+ *    stream order and works on without it; the word is never cleared by
+ *    these calls, so the caller zeroes it once and looks when it likes.
+ *  - A device other than compute capability 10.0 gives MK_ERR_INVALID, a
+ *    failed launch MK_ERR_CUDA.
+ */
+enum mk_dtype { MK_BF16 = 0, MK_FP16 = 1 };
+
+/* The most query heads per KV head these operators take (any whole number
+ * up to it), and the largest vocabulary mk_sample takes. */
+#define MK_MAX_GROUP 8
+#define MK_MAX_VOCAB (1 << 20)
+
+/*
+ * A paged KV cache of one layer.
+ *   k, v        device [num_pages][n_kv_heads][page_size][head_dim], dtype;
+ *               keys are stored after RoPE.  page_size is any number of
+ *               positions >= 1 (attention is fastest at multiples of 16).
+ *   page_table  device int32 [n_seqs][pages_per_seq]: position p of sequence
+ *               s is row p % page_size of page page_table[s][p / page_size].
+ *               Sequences may share pages they only read.  Only the entries
+ *               of positions a call reads or writes are looked at.
+ * head_dim is 64 or 128.  The cache of a context (mk_kv: [max_batch]
+ * [n_kv_heads][max_seq][head_dim]) is a paged cache of max_batch pages of
+ * max_seq positions whose table names page b for sequence b.
+ */
+typedef struct mk_paged_kv {
+    void *k, *v;
+    const int32_t *page_table;
+    int n_seqs, pages_per_seq;
+    int num_pages, page_size;
+    int n_kv_heads, head_dim;
+    int dtype;
+} mk_paged_kv;
+
+/*
+ * Append the keys and values of new tokens to a paged cache, rotating q and
+ * k on the way (the half-split rotary embedding of the decode step: for
+ * i < head_dim / 2 the pair (x[i], x[i + head_dim / 2]) turns by position *
+ * rope_theta^(-2i / head_dim); angles in 64 bits, the rotation in 32, one
+ * rounding to dtype).
+ *   cu_tokens  device int32 [n_seqs + 1]: rows cu_tokens[s] ..
+ *              cu_tokens[s + 1] - 1 are sequence s's new tokens (none is
+ *              fine), cu_tokens[0] = 0.  For one token per sequence it counts
+ *              0, 1, 2, ...
+ *   start_pos  device int32 [n_seqs]: position of the sequence's first new
+ *              token; the others follow.
+ *   n_tokens   rows of q, k and v; rows from cu_tokens[n_seqs] on are neither
+ *              read nor written.
+ *   q, q_out   [n_tokens][n_q_heads][head_dim]; both NULL (n_q_heads = 0):
+ *              only k is rotated.  q_out may be q.
+ *   k, v       [n_tokens][n_kv_heads][head_dim].
+ *   k_out      rotated k as rows, for mk_prompt_attention (may be k), or NULL.
+ * A token whose position lies outside the table (negative, or beyond
+ * pages_per_seq * page_size) or on a page outside [0, num_pages) is a bad
+ * value: its row is left out, outputs included.  Two tokens of one call
+ * must not fall on the same cache row (shared pages).  Input and output rows
+ * must not overlap except for the in-place forms named above.
+ */
+int mk_kv_append(const mk_paged_kv *kv, const int32_t *cu_tokens, const int32_t *start_pos, int n_tokens,
+                 int n_q_heads, const void *q, long long q_stride, const void *k, long long k_stride,
+                 const void *v, long long v_stride, float rope_theta, void *q_out, long long q_out_stride,
+                 void *k_out, long long k_out_stride, int32_t *status_out, mk_stream_t stream);
+
+/*
+ * Attention of one token per sequence over a paged cache: for query head i
+ * of sequence s, with h = i / (n_q_heads / n_kv_heads),
+ *   out[s][i] = sum_j softmax_j(scale * q[s][i] . k[j][h]) v[j][h],
+ *   j < kv_lens[s].
+ * A sequence of length 0 gives zeros.  Positions from kv_lens[s] on are not
+ * read.
+ *   kv_lens   device int32 [n_seqs]
+ *   max_len   host bound on kv_lens (at most pages_per_seq * page_size): it
+ *             sizes the launch and the workspace, so that the same launch can
+ *             be replayed while the lengths grow up to it.
+ *   q, out    [n_seqs][n_q_heads][head_dim], the cache's dtype
+ *   scale     > 0; usually 1 / sqrt(head_dim)
+ *   workspace device, 16-byte aligned, at least the bytes
+ *             mk_paged_attention_workspace reports; its contents need not be
+ *             initialised and mean nothing afterwards.  Calls (or graph
+ *             replays) that may overlap on the device need one each.
+ * Softmax statistics and sums are 32-bit.  Bad values: a length outside
+ * [0, max_len] is clamped to it; positions on a page outside [0, num_pages)
+ * are left out of the sums.
+ */
+int mk_paged_attention(const mk_paged_kv *kv, const int32_t *kv_lens, int max_len, int n_q_heads, const void *q,
+                       long long q_stride, float scale, void *out, long long out_stride, void *workspace,
+                       size_t workspace_bytes, int32_t *status_out, mk_stream_t stream);
+
+/* Bytes of workspace mk_paged_attention needs on the current device for
+ * these sizes (*bytes_out; 0 is possible, the workspace may then be NULL).
+ * The pointers of *kv are not looked at. */
+int mk_paged_attention_workspace(const mk_paged_kv *kv, int max_len, int n_q_heads, size_t *bytes_out);
+
+/*
+ * Causal attention over packed prompts: token t of sequence s attends to the
+ * sequence's tokens up to and including itself, with grouped heads as in
+ * mk_paged_attention.
+ *   cu_seqlens  device int32 [n_seqs + 1]: sequence s is rows cu_seqlens[s] ..
+ *               cu_seqlens[s + 1] - 1 (none is fine), cu_seqlens[0] = 0.
+ *   n_tokens    rows of the buffers; rows of `out` from cu_seqlens[n_seqs] on
+ *               are left as they were.
+ *   max_len     host bound on the sequence lengths (sizes the launch).
+ *   q, out      [n_tokens][n_q_heads][head_dim]; k, v [n_tokens][n_kv_heads]
+ *               [head_dim]; all of `dtype`.  out must not overlap q, k or v.
+ * Values of later tokens or other sequences never reach a row, whatever they
+ * hold (NaN and infinities included).  Scores, statistics and sums are
+ * 32-bit; the softmax weights enter the value product in `dtype`.  Bad
+ * values: a sequence whose rows are not 0 <= cu_seqlens[s] <=
+ * cu_seqlens[s + 1] <= n_tokens or that is longer than max_len is left out
+ * (its rows of out are not written; where cu_seqlens decreases, rows that two
+ * sequences claim hold either's value).
+ */
+int mk_prompt_attention(int dtype, int n_q_heads, int n_kv_heads, int head_dim, const int32_t *cu_seqlens,
+                        int n_seqs, int n_tokens, int max_len, const void *q, long long q_stride, const void *k,
+                        long long k_stride, const void *v, long long v_stride, float scale, void *out,
+                        long long out_stride, int32_t *status_out, mk_stream_t stream);
+
+/*
+ * Sample one token per row of logits, from given uniform random numbers.
+ * With m the largest logit and w_i = exp((l_i - m) / temperature):
+ *   1. keep the top_k largest logits (lowest index first on ties);
+ *   2. of those, in descending order (lowest index first on ties), keep the
+ *      shortest prefix that holds top_p of their summed w, at least one;
+ *   3. of those keep w_i >= min_p;
+ *   4. the token is the first kept index, in index order, at which the
+ *      running sum of w exceeds uniform * (sum over all kept).
+ * Weights are computed in 64 bits and summed as 64-bit integers (in units of
+ * 2^-43 of the largest), so the result does not depend on any order of
+ * summation; weights below that unit count as zero.
+ *   logits       device float [rows][vocab], row_stride (>= vocab) elements
+ *                between rows; vocab <= MK_MAX_VOCAB
+ *   uniform      device float [rows], in [0, 1) (values outside are clamped)
+ *   temperature  device float [rows]; not above 0: the row's argmax (lowest
+ *                index), the filters and uniform unused.  NULL: 1.
+ *   top_k        device int32 [rows]; not above 0 or >= vocab: off.  NULL: off.
+ *   top_p        device float [rows]; >= 1 or NaN: off; at most 0: only the
+ *                largest.  NULL: off.
+ *   min_p        device float [rows]; not above 0: off; above 1 counts as 1.
+ *                NULL: off.
+ *   token_out    device int32 [rows]
+ * Logits of -infinity and NaN are never chosen; a row with nothing else gives
+ * -1 (which mk_decode_step refuses).  +infinity takes all the weight, shared
+ * among its equals.
+ */
+int mk_sample(const float *logits, long long row_stride, int rows, int vocab, const float *uniform,
+              const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+              int32_t *token_out, mk_stream_t stream);
+
 /* Test hook: overwrite the threshold of one event (simulates a graph
  * whose event can never fire; the next step then ends in MK_ERR_TIMEOUT).
  * Blocks the host. */

@@ -1,0 +1,67 @@
+// mk_ops.h -- host-side interface between the serving operators' C entry
+// points (mk_ops.cpp: argument checks) and their launchers (mk_kv_append.cu,
+// mk_paged_attn.cu, mk_prompt_attn.cu, mk_sample.cu).  Not part of the public
+// ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/mk.h"
+
+namespace mk {
+
+constexpr int kOpsMaxDevices = 64;
+
+struct AppendArgs {
+    mk_paged_kv kv;
+    const int32_t *cu, *start;
+    int n_tokens, n_q_heads;
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;
+    float theta;
+    void *q_out, *k_out;
+    long long q_out_stride, k_out_stride;
+    int32_t *status;
+};
+cudaError_t append_launch(const AppendArgs &a, cudaStream_t stream);
+
+struct PagedArgs {
+    mk_paged_kv kv;
+    const int32_t *lens;
+    int max_len, n_q_heads;
+    const void *q;
+    void *out;
+    long long q_stride, out_stride;
+    float scale;
+    void *workspace;
+    int32_t *status;
+};
+size_t paged_workspace(const mk_paged_kv &kv, int max_len, int n_q_heads, int num_sms);
+cudaError_t paged_launch(const PagedArgs &a, int device, int num_sms, cudaStream_t stream);
+
+struct PromptArgs {
+    int dtype, nq, nkv, d;
+    const int32_t *cu;
+    int n_seqs, n_tokens, max_len;
+    const void *q, *k, *v;
+    void *out;
+    long long q_stride, k_stride, v_stride, out_stride;
+    float scale;
+    int32_t *status;
+};
+cudaError_t prompt_launch(const PromptArgs &a, int device, int num_sms, cudaStream_t stream);
+
+struct SampleArgs {
+    const float *logits;
+    long long stride;
+    int rows, vocab;
+    const float *uniform, *temperature;
+    const int32_t *top_k;
+    const float *top_p, *min_p;
+    int32_t *token;
+};
+cudaError_t sample_launch(const SampleArgs &a, int device, int num_sms, cudaStream_t stream);
+
+}  // namespace mk

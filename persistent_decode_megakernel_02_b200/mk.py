@@ -26,6 +26,9 @@ MK_FLAG_ATTN_KV_ITEMS = 32
 MK_FLAG_ATTN_Q_ITEMS = 64
 MAX_BATCH = 16
 MK_BUF_HIDDEN, MK_BUF_Q, MK_BUF_ATTN, MK_BUF_ACT = range(4)
+MK_BF16, MK_FP16 = range(2)
+MAX_GROUP = 8
+MAX_VOCAB = 1 << 20
 OP_NAMES = ["qkv", "attn", "oproj", "gateup", "down", "lmhead"]
 
 if not os.path.exists(LIB_PATH):
@@ -79,6 +82,13 @@ class Info(C.Structure):
                 ("err_task", C.c_uint), ("attn_heads", C.c_int)]
 
 
+class PagedKVStruct(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("page_table", C.c_void_p),
+                ("n_seqs", C.c_int), ("pages_per_seq", C.c_int), ("num_pages", C.c_int),
+                ("page_size", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("dtype", C.c_int)]
+
+
 class TraceRec(C.Structure):
     _fields_ = [("t_ready", C.c_ulonglong), ("t_start", C.c_ulonglong), ("t_input", C.c_ulonglong),
                 ("t_done", C.c_ulonglong), ("t_end", C.c_ulonglong), ("t_wait", C.c_ulonglong),
@@ -107,6 +117,18 @@ _lib.mk_generate.argtypes = [_P, _P, C.c_int, _P, C.c_int, C.c_int, C.c_int, _P,
 _lib.mk_prefill.argtypes = [_P, _P, C.c_int, C.c_int, C.c_int, _P, _P, _P]
 _lib.mk_decode_step_static.argtypes = [C.POINTER(Config), C.POINTER(PackedWeights), C.POINTER(KV),
                                        _P, _P, C.c_int, _P, _P, _P, _P]
+_LL = C.c_longlong
+_lib.mk_kv_append.argtypes = [C.POINTER(PagedKVStruct), _P, _P, C.c_int, C.c_int, _P, _LL, _P, _LL, _P, _LL,
+                              C.c_float, _P, _LL, _P, _LL, _P, _P]
+_lib.mk_paged_attention.argtypes = [C.POINTER(PagedKVStruct), _P, C.c_int, C.c_int, _P, _LL, C.c_float, _P, _LL,
+                                    _P, C.c_size_t, _P, _P]
+_lib.mk_paged_attention_workspace.argtypes = [C.POINTER(PagedKVStruct), C.c_int, C.c_int, C.POINTER(C.c_size_t)]
+_lib.mk_prompt_attention.argtypes = [C.c_int, C.c_int, C.c_int, C.c_int, _P, C.c_int, C.c_int, C.c_int, _P, _LL,
+                                     _P, _LL, _P, _LL, C.c_float, _P, _LL, _P, _P]
+_lib.mk_sample.argtypes = [_P, _LL, C.c_int, C.c_int, _P, _P, _P, _P, _P, _P, _P]
+for _f in ("mk_kv_append", "mk_paged_attention", "mk_paged_attention_workspace", "mk_prompt_attention",
+           "mk_sample"):
+    getattr(_lib, _f).restype = C.c_int
 for _f in ("mk_create", "mk_decode_step", "mk_sync", "mk_reset", "mk_destroy", "mk_get_info",
            "mk_get_event_counts", "mk_read_buffer", "mk_get_trace", "mk_get_graph", "mk_plan",
            "mk_get_sm_stats", "mk_decode_step_static",
@@ -345,3 +367,225 @@ class Context:
 
     def debug_withhold_event(self, event: int):
         _check(_lib.mk_debug_withhold_event(self._h, int(event)), "mk_debug_withhold_event")
+
+    def paged_kv(self, layer: int) -> "PagedKV":
+        """The context's cache of one layer as a paged cache: max_batch pages
+        of max_seq positions, page b for sequence b.  What the operators append
+        the context's steps read, and the other way round."""
+        k, v = self._keep[1][layer], self._keep[2][layer]
+        import torch
+        table = torch.arange(self.cfg.max_batch, dtype=torch.int32, device=k.device)[:, None]
+        shape = (self.cfg.max_batch, self.cfg.n_kv_heads, self.cfg.max_seq, self.cfg.head_dim)
+        return PagedKV(k.view(shape), v.view(shape), table)
+
+
+# ---- serving operators (no context) -----------------------------------------
+#
+# Each checks its tensors (device, type, layout) here, because the library
+# sees pointers only; what it finds wrong is an MkError of MK_ERR_INVALID, as
+# are the library's own refusals.  The tensors' device is made current for
+# the call; stream=None means that device's current stream.
+
+def _invalid(what: str, why: str):
+    raise MkError(MK_ERR_INVALID, f"{what}: {why}")
+
+
+def _dtype_code(dtype) -> int:
+    import torch
+    return MK_BF16 if dtype is torch.bfloat16 else MK_FP16 if dtype is torch.float16 else -1
+
+
+def _rows(what: str, name: str, t, dtype, device, rows: int, heads: int, d: int) -> int:
+    """Stride between the tokens of a [rows][heads][d] tensor whose heads are
+    contiguous."""
+    if t.dtype is not dtype or t.device != device:
+        _invalid(what, f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != heads or t.shape[2] != d:
+        _invalid(what, f"{name} must be [{rows}][{heads}][{d}], got {list(t.shape)}")
+    st = t.stride()
+    if rows and (st[2] != 1 or (heads > 1 and st[1] != d)):
+        _invalid(what, f"{name}'s heads must be contiguous")
+    return st[0] if rows > 1 else max(st[0], heads * d) // 8 * 8
+
+
+def _vec(what: str, name: str, t, dtype, device, n: int):
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.device != device or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        _invalid(what, f"{name} must be a contiguous {dtype} vector of {n} on {device}, "
+                       f"got {t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _status_ptr(what: str, t, device):
+    import torch
+    return _vec(what, "status", t, torch.int32, device, 1)
+
+
+class _On:
+    """Makes a device current for a call when it is not."""
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        import torch
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _stream_on(what: str, stream, device):
+    """The raw stream of a call: the given one, or the device's current one."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device.index) or None
+    if stream.device != device:
+        _invalid(what, f"the stream is on {stream.device}, the tensors on {device}")
+    return int(stream.cuda_stream) or None
+
+
+class PagedKV:
+    """A paged KV cache of one layer (mk_paged_kv): k, v CUDA tensors
+    [num_pages][n_kv_heads][page_size][head_dim] of bf16 or fp16, page_table
+    int32 [n_seqs][pages_per_seq].  Holds the tensors it names."""
+
+    def __init__(self, k, v, page_table):
+        import torch
+        what = "PagedKV"
+        if k.dim() != 4 or _dtype_code(k.dtype) < 0 or not k.is_cuda or not k.is_contiguous():
+            _invalid(what, "k must be a contiguous bf16 or fp16 CUDA tensor "
+                           "[num_pages][n_kv_heads][page_size][head_dim]")
+        if v.dtype is not k.dtype or v.device != k.device or v.shape != k.shape or not v.is_contiguous():
+            _invalid(what, "v must be laid out like k")
+        if (page_table.dim() != 2 or page_table.dtype is not torch.int32 or page_table.device != k.device
+                or not page_table.is_contiguous()):
+            _invalid(what, "page_table must be a contiguous int32 [n_seqs][pages_per_seq] on k's device")
+        self.k, self.v, self.page_table = k, v, page_table
+        self.dtype, self.device = k.dtype, k.device
+        self.n_seqs, self.pages_per_seq = page_table.shape
+        self.num_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        self._st = PagedKVStruct(_ptr(k), _ptr(v), _ptr(page_table), self.n_seqs, self.pages_per_seq,
+                                 self.num_pages, self.page_size, self.n_kv_heads, self.head_dim,
+                                 _dtype_code(k.dtype))
+        self._ref = C.byref(self._st)
+
+
+def kv_append(cache: PagedKV, q, k, v, cu_tokens, start_pos, rope_theta: float, q_out=None, k_out=None,
+              status=None, stream=None):
+    """mk_kv_append: rotate q and k, write k and v to the cache.  q [n][n_q_heads][d]
+    (or None: k only), k, v [n][n_kv_heads][d], cu_tokens int32 [n_seqs + 1],
+    start_pos int32 [n_seqs].  q_out (default: in place) receives the rotated
+    q, k_out (default: not kept) the rotated k as rows."""
+    import torch
+    what, dev, dt, n, d = "kv_append", cache.device, cache.dtype, k.shape[0], cache.head_dim
+    ks = _rows(what, "k", k, dt, dev, n, cache.n_kv_heads, d)
+    vs = _rows(what, "v", v, dt, dev, n, cache.n_kv_heads, d)
+    nq = qs = qos = kos = 0
+    if q is not None:
+        nq = q.shape[1] if q.dim() == 3 else 0
+        q_out = q if q_out is None else q_out
+        qs = _rows(what, "q", q, dt, dev, n, nq, d)
+        qos = _rows(what, "q_out", q_out, dt, dev, n, nq, d)
+    elif q_out is not None:
+        _invalid(what, "q_out without q")
+    if k_out is not None:
+        kos = _rows(what, "k_out", k_out, dt, dev, n, cache.n_kv_heads, d)
+    cu = _vec(what, "cu_tokens", cu_tokens, torch.int32, dev, cache.n_seqs + 1)
+    sp = _vec(what, "start_pos", start_pos, torch.int32, dev, cache.n_seqs)
+    if n == 0:
+        return
+    with _On(dev):
+        _check(_lib.mk_kv_append(cache._ref, cu, sp, n, nq, q.data_ptr() if nq else None, qs, k.data_ptr(), ks,
+                                 v.data_ptr(), vs, rope_theta, q_out.data_ptr() if nq else None, qos,
+                                 k_out.data_ptr() if k_out is not None else None, kos,
+                                 _status_ptr(what, status, dev), _stream_on(what, stream, dev)), "mk_kv_append")
+
+
+def paged_attention_workspace(cache: PagedKV, n_q_heads: int, max_len: int):
+    """A workspace for paged_attention calls of these sizes (uint8 CUDA tensor;
+    calls that may overlap on the device need one each)."""
+    import torch
+    n = C.c_size_t()
+    with _On(cache.device):
+        _check(_lib.mk_paged_attention_workspace(cache._ref, max_len, n_q_heads, C.byref(n)),
+               "mk_paged_attention_workspace")
+    return torch.empty(n.value, dtype=torch.uint8, device=cache.device)
+
+
+def paged_attention(cache: PagedKV, q, kv_lens, max_len: int, out, workspace=None, scale=None, status=None,
+                    stream=None):
+    """mk_paged_attention: one token per sequence over the cache.  q, out
+    [n_seqs][n_q_heads][d]; kv_lens int32 [n_seqs], at most max_len (a host
+    number); scale defaults to 1 / sqrt(d).  Without a workspace one is
+    allocated for the call on its stream."""
+    import torch
+    what, dev, dt, d = "paged_attention", cache.device, cache.dtype, cache.head_dim
+    nq = q.shape[1] if q.dim() == 3 else 0
+    qs = _rows(what, "q", q, dt, dev, cache.n_seqs, nq, d)
+    os_ = _rows(what, "out", out, dt, dev, cache.n_seqs, nq, d)
+    lens = _vec(what, "kv_lens", kv_lens, torch.int32, dev, cache.n_seqs)
+    if workspace is None:
+        if stream is None:
+            workspace = paged_attention_workspace(cache, nq, max_len)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = paged_attention_workspace(cache, nq, max_len)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        _invalid(what, "workspace must be contiguous on the cache's device")
+    with _On(dev):
+        _check(_lib.mk_paged_attention(cache._ref, lens, max_len, nq, q.data_ptr(), qs,
+                                       d ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+                                       workspace.data_ptr() or None, workspace.numel() * workspace.element_size(),
+                                       _status_ptr(what, status, dev), _stream_on(what, stream, dev)),
+               "mk_paged_attention")
+
+
+def prompt_attention(q, k, v, cu_seqlens, max_len: int, out, scale=None, status=None, stream=None):
+    """mk_prompt_attention: causal attention over packed prompts.  q, out
+    [n][n_q_heads][d], k, v [n][n_kv_heads][d], cu_seqlens int32 [n_seqs + 1],
+    max_len a host bound on the lengths; scale defaults to 1 / sqrt(d)."""
+    import torch
+    what, dev, dt = "prompt_attention", q.device, q.dtype
+    if q.dim() != 3 or k.dim() != 3 or not q.is_cuda or _dtype_code(dt) < 0:
+        _invalid(what, "q and k must be [n][heads][d] CUDA tensors of bf16 or fp16")
+    n, nq, d = q.shape
+    nkv = k.shape[1]
+    qs = _rows(what, "q", q, dt, dev, n, nq, d)
+    ks = _rows(what, "k", k, dt, dev, n, nkv, d)
+    vs = _rows(what, "v", v, dt, dev, n, nkv, d)
+    os_ = _rows(what, "out", out, dt, dev, n, nq, d)
+    ns = cu_seqlens.shape[0] - 1 if cu_seqlens.dim() == 1 else 0
+    cu = _vec(what, "cu_seqlens", cu_seqlens, torch.int32, dev, ns + 1)
+    if n == 0:
+        return
+    with _On(dev):
+        _check(_lib.mk_prompt_attention(_dtype_code(dt), nq, nkv, d, cu, ns, n, max_len, q.data_ptr(), qs,
+                                        k.data_ptr(), ks, v.data_ptr(), vs, d ** -0.5 if scale is None else scale,
+                                        out.data_ptr(), os_, _status_ptr(what, status, dev),
+                                        _stream_on(what, stream, dev)), "mk_prompt_attention")
+
+
+def sample(logits, uniform, token_out, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """mk_sample: one token per row of float32 logits [rows][vocab] (rows may
+    be strided) from the given uniform numbers; the parameters are vectors of
+    one value per row, or None (temperature 1, filter off)."""
+    import torch
+    what, dev = "sample", logits.device
+    if logits.dim() != 2 or logits.dtype is not torch.float32 or not logits.is_cuda or \
+            (logits.shape[1] > 1 and logits.stride(1) != 1):
+        _invalid(what, "logits must be a float32 CUDA tensor [rows][vocab] with contiguous rows")
+    rows, vocab = logits.shape
+    f, i = torch.float32, torch.int32
+    args = (_vec(what, "uniform", uniform, f, dev, rows), _vec(what, "temperature", temperature, f, dev, rows),
+            _vec(what, "top_k", top_k, i, dev, rows), _vec(what, "top_p", top_p, f, dev, rows),
+            _vec(what, "min_p", min_p, f, dev, rows), _vec(what, "token_out", token_out, i, dev, rows))
+    if rows == 0:
+        return
+    with _On(dev):
+        _check(_lib.mk_sample(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, rows, vocab, *args,
+                              _stream_on(what, stream, dev)), "mk_sample")

@@ -1,0 +1,151 @@
+"""Refusals of the serving operators (no GPU): every argument the host can
+see is checked before the device is touched, so made-up pointers are never
+followed."""
+import ctypes as C
+import math
+
+import pytest
+
+mk = pytest.importorskip("persistent_decode_megakernel_02_b200.mk")
+lib = mk._lib
+A = 1 << 20          # an aligned made-up address
+
+
+def cache(**kw):
+    f = dict(k=A, v=A, page_table=A, n_seqs=2, pages_per_seq=4, num_pages=8, page_size=16, n_kv_heads=2,
+             head_dim=64, dtype=mk.MK_BF16)
+    f.update(kw)
+    return mk.PagedKVStruct(**f)
+
+
+BAD_CACHES = [dict(k=None), dict(v=A + 8), dict(page_table=None), dict(page_table=A + 2), dict(n_seqs=0),
+              dict(pages_per_seq=0), dict(num_pages=0), dict(page_size=0), dict(page_size=-1), dict(n_kv_heads=0),
+              dict(head_dim=96), dict(head_dim=0), dict(dtype=2), dict(dtype=-1),
+              dict(pages_per_seq=1 << 20, page_size=1 << 20)]
+
+
+def append(c=None, **kw):
+    a = dict(cu=A, start=A, n=4, nq=4, q=A, qs=256, k=A, ks=128, v=A, vs=128, theta=1e4, qo=A, qos=256, ko=None,
+             kos=0, status=None)
+    a.update(kw)
+    c = cache() if c is None else c
+    return lib.mk_kv_append(C.byref(c), a["cu"], a["start"], a["n"], a["nq"], a["q"], a["qs"], a["k"], a["ks"],
+                            a["v"], a["vs"], a["theta"], a["qo"], a["qos"], a["ko"], a["kos"], a["status"], None)
+
+
+def paged(c=None, **kw):
+    a = dict(lens=A, max_len=64, nq=4, q=A, qs=256, scale=0.125, out=A, os=256, ws=A, wsb=1 << 40, status=None)
+    a.update(kw)
+    c = cache() if c is None else c
+    return lib.mk_paged_attention(C.byref(c), a["lens"], a["max_len"], a["nq"], a["q"], a["qs"], a["scale"],
+                                  a["out"], a["os"], a["ws"], a["wsb"], a["status"], None)
+
+
+def prompt(**kw):
+    a = dict(dtype=mk.MK_FP16, nq=4, nkv=2, d=64, cu=A, ns=2, n=10, max_len=8, q=A, qs=256, k=A, ks=128, v=A,
+             vs=128, scale=0.125, out=A, os=256, status=None)
+    a.update(kw)
+    return lib.mk_prompt_attention(a["dtype"], a["nq"], a["nkv"], a["d"], a["cu"], a["ns"], a["n"], a["max_len"],
+                                   a["q"], a["qs"], a["k"], a["ks"], a["v"], a["vs"], a["scale"], a["out"], a["os"],
+                                   a["status"], None)
+
+
+def sample(**kw):
+    a = dict(logits=A, stride=100, rows=2, vocab=100, u=A, t=A, k=A, p=A, m=A, out=A)
+    a.update(kw)
+    return lib.mk_sample(a["logits"], a["stride"], a["rows"], a["vocab"], a["u"], a["t"], a["k"], a["p"], a["m"],
+                         a["out"], None)
+
+
+@pytest.mark.parametrize("bad", BAD_CACHES, ids=str)
+def test_caches_are_checked(bad):
+    assert append(cache(**bad)) == mk.MK_ERR_INVALID
+    assert paged(cache(**bad)) == mk.MK_ERR_INVALID
+
+
+@pytest.mark.parametrize("bad", [
+    dict(cu=None), dict(cu=A + 1), dict(start=None), dict(n=-1), dict(nq=3), dict(nq=18), dict(nq=-2),
+    dict(q=None), dict(q=A + 2), dict(qs=248), dict(qs=260), dict(qs=0), dict(k=None), dict(ks=120), dict(ks=132),
+    dict(v=A + 8), dict(vs=64), dict(theta=1.0), dict(theta=math.nan), dict(theta=math.inf), dict(qo=None),
+    dict(qos=128), dict(ko=A + 4, kos=128), dict(ko=A, kos=64), dict(nq=0), dict(nq=0, q=None),
+    dict(q=A, qo=A, qs=256, qos=512), dict(ko=A, kos=256), dict(status=A + 2)], ids=str)
+def test_append_refusals(bad):
+    assert append(**bad) == mk.MK_ERR_INVALID
+
+
+@pytest.mark.parametrize("bad", [
+    dict(lens=None), dict(lens=A + 2), dict(max_len=-1), dict(max_len=65), dict(nq=3), dict(nq=0), dict(nq=18),
+    dict(q=None), dict(q=A + 8), dict(qs=128), dict(qs=257), dict(scale=0.0), dict(scale=-1.0),
+    dict(scale=math.nan), dict(scale=math.inf), dict(out=None), dict(os=8), dict(ws=A + 8), dict(status=A + 1)],
+    ids=str)
+def test_paged_refusals(bad):
+    assert paged(**bad) == mk.MK_ERR_INVALID
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=2), dict(nq=5), dict(nq=0), dict(nkv=0), dict(nq=18), dict(d=80), dict(d=256), dict(cu=None),
+    dict(cu=A + 2), dict(ns=0), dict(n=-1), dict(max_len=-1), dict(q=None), dict(qs=255), dict(qs=0), dict(k=A + 2),
+    dict(ks=64), dict(v=None), dict(vs=129), dict(scale=0.0), dict(scale=math.nan), dict(out=None), dict(os=192),
+    dict(status=A + 3)], ids=str)
+def test_prompt_refusals(bad):
+    assert prompt(**bad) == mk.MK_ERR_INVALID
+
+
+@pytest.mark.parametrize("bad", [
+    dict(logits=None), dict(logits=A + 2), dict(stride=99), dict(rows=-1), dict(vocab=0), dict(u=None),
+    dict(vocab=mk.MAX_VOCAB + 1, stride=1 << 21), dict(out=None), dict(out=A + 1), dict(t=A + 2), dict(k=A + 1),
+    dict(p=A + 3), dict(m=A + 2)], ids=str)
+def test_sample_refusals(bad):
+    assert sample(**bad) == mk.MK_ERR_INVALID
+
+
+def test_workspace_refusals():
+    n = C.c_size_t(7)
+    ask = lambda c, m, nq: lib.mk_paged_attention_workspace(C.byref(c), m, nq, C.byref(n))
+    for c, m, nq in ((cache(head_dim=32), 10, 4), (cache(), 65, 4), (cache(), -1, 4), (cache(), 10, 5),
+                     (cache(), 10, 0)):
+        assert ask(c, m, nq) == mk.MK_ERR_INVALID and n.value == 0
+    assert lib.mk_paged_attention_workspace(None, 1, 1, C.byref(n)) == mk.MK_ERR_INVALID
+    assert lib.mk_paged_attention_workspace(C.byref(cache()), 1, 4, None) == mk.MK_ERR_INVALID
+
+
+def test_nothing_to_do_touches_no_device():
+    assert append(n=0) == mk.MK_OK
+    assert prompt(n=0) == mk.MK_OK
+    assert sample(rows=0) == mk.MK_OK
+
+
+def test_null_cache():
+    assert lib.mk_kv_append(None, A, A, 1, 0, None, 0, A, 128, A, 128, 1e4, None, 0, None, 0, None, None) \
+        == mk.MK_ERR_INVALID
+    assert lib.mk_paged_attention(None, A, 1, 4, A, 256, 1.0, A, 256, A, 1 << 30, None, None) == mk.MK_ERR_INVALID
+
+
+def test_cache_struct_matches_the_c_compiler(tmp_path):
+    import shutil
+    import subprocess
+    if shutil.which("gcc") is None:
+        pytest.skip("needs gcc")
+    lines = ["#include <stdio.h>", "#include <stddef.h>", f'#include "{mk.HEADER_PATH}"', "int main(void) {",
+             'printf("%zu\\n", sizeof(mk_paged_kv));']
+    names = [n for n, _ in mk.PagedKVStruct._fields_]
+    lines += [f'printf("%zu\\n", offsetof(mk_paged_kv, {n}));' for n in names]
+    lines += ['printf("%d\\n", MK_MAX_GROUP);', 'printf("%d\\n", MK_MAX_VOCAB);', "return 0;", "}"]
+    src, exe = tmp_path / "t.c", tmp_path / "t"
+    src.write_text("\n".join(lines))
+    subprocess.check_call(["gcc", "-std=c11", "-o", str(exe), str(src)])
+    got = [int(x) for x in subprocess.check_output([str(exe)], text=True).split()]
+    want = [C.sizeof(mk.PagedKVStruct)] + [getattr(mk.PagedKVStruct, n).offset for n in names]
+    assert got == want + [mk.MAX_GROUP, mk.MAX_VOCAB]
+
+
+def test_binding_checks_its_tensors():
+    import torch
+    k = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(mk.MkError) as e:      # not on a GPU
+        mk.PagedKV(k, k, torch.zeros(1, 2, dtype=torch.int32))
+    assert e.value.status == mk.MK_ERR_INVALID
+    with pytest.raises(mk.MkError):
+        mk.sample(torch.zeros(1, 8), torch.zeros(1), torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(mk.MkError):
+        mk.prompt_attention(k[0], k[0], k[0], torch.zeros(2, dtype=torch.int32), 4, k[0])
