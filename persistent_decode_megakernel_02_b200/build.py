@@ -15,7 +15,7 @@ LIB = os.path.join(HERE, "libmk.so")
 SOURCES = ["mk_kernel.cu", "mk_runtime.cpp", "mk_graph.cpp", "mk_static.cu", "mk_rows.cu",
            "mk_rows_graph.cpp", "mk_rows_runtime.cpp", "mk_ops.cpp", "mk_kv_append.cu",
            "mk_paged_attn.cu", "mk_prompt_attn.cu", "mk_sample.cu"]
-HEADERS = ["mk_internal.h", "mk_ptx.cuh", "mk_rows.h", "mk_ops.h", "mk_ops.cuh"]
+HEADERS = ["mk_internal.h", "mk_ptx.cuh", "mk_rows.h", "mk_ops.h", "mk_ops.cuh", "mk_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

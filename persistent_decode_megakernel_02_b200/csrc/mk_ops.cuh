@@ -14,6 +14,7 @@ namespace mk {
 // Two 16-bit elements of a 32-bit word, widened; and back, each rounded to
 // nearest even.
 struct Bf16 {
+    static constexpr bool kBf16 = true;
     static __device__ __forceinline__ float2 unpack(uint32_t w) { return make_float2(bf_lo(w), bf_hi(w)); }
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -21,6 +22,7 @@ struct Bf16 {
     }
 };
 struct Fp16 {
+    static constexpr bool kBf16 = false;
     static __device__ __forceinline__ float2 unpack(uint32_t w) {
         return __half22float2(*reinterpret_cast<const __half2 *>(&w));
     }
