@@ -533,7 +533,8 @@ enum mk_dtype { MK_BF16 = 0, MK_FP16 = 1 };
  *               s is row p % page_size of page page_table[s][p / page_size].
  *               Sequences may share pages they only read.  Only the entries
  *               of positions a call reads or writes are looked at.
- * head_dim is 64 or 128.  The cache of a context (mk_kv: [max_batch]
+ * head_dim is 64 or 128; num_pages * n_kv_heads * page_size is at most
+ * 2^31 - 1.  The cache of a context (mk_kv: [max_batch]
  * [n_kv_heads][max_seq][head_dim]) is a paged cache of max_batch pages of
  * max_seq positions whose table names page b for sequence b.
  */
@@ -589,9 +590,10 @@ int mk_kv_append(const mk_paged_kv *kv, const int32_t *cu_tokens, const int32_t 
  *   q, out    [n_seqs][n_q_heads][head_dim], the cache's dtype
  *   scale     > 0; usually 1 / sqrt(head_dim)
  *   workspace device, 16-byte aligned, at least the bytes
- *             mk_paged_attention_workspace reports; its contents need not be
- *             initialised and mean nothing afterwards.  Calls (or graph
- *             replays) that may overlap on the device need one each.
+ *             mk_paged_attention_workspace reports, filled with zeros once
+ *             before its first use; every call leaves it ready for the next
+ *             one, of these or other sizes.  Calls (or graph replays) that may
+ *             overlap on the device need one each.
  * Softmax statistics and sums are 32-bit.  Bad values: a length outside
  * [0, max_len] is clamped to it; positions on a page outside [0, num_pages)
  * are left out of the sums.

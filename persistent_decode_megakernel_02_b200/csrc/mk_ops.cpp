@@ -29,7 +29,9 @@ bool cache_sizes_ok(const mk_paged_kv *kv) {
     return kv && kv->n_seqs >= 1 && kv->pages_per_seq >= 1 && kv->num_pages >= 1 && kv->page_size >= 1 &&
            kv->n_kv_heads >= 1 && kv->n_kv_heads <= (1 << 16) && (kv->head_dim == 64 || kv->head_dim == 128) &&
            (kv->dtype == MK_BF16 || kv->dtype == MK_FP16) &&
-           (long long)kv->pages_per_seq * kv->page_size <= 0x7fffff00LL;
+           (long long)kv->pages_per_seq * kv->page_size <= 0x7fffff00LL &&
+           // rows of the cache fit an int (more would not fit the device)
+           (double)kv->num_pages * kv->n_kv_heads * kv->page_size <= 2147483647.0;
 }
 
 bool cache_ok(const mk_paged_kv *kv) {

@@ -1,106 +1,454 @@
 // mk_paged_attn.cu -- attention of one new token per sequence over a paged
-// cache.
+// cache, split over the caches' length and joined in the same launch.
 //
-// One block per (sequence, KV head): its warps take the positions in turn,
-// scoring the KV head's query heads against each key, with a running maximum
-// and sum per warp and head; the warps' states are merged at the end.
+// Every key and value is read once for the G query heads of its KV head; 4 G
+// flops per 4 bytes, so the kernel is bound by memory as long as enough bytes
+// are in flight.  The work of all (sequence, KV head) items is laid end to
+// end in steps of 8 KB of cache and cut into equal ranges, one per block:
+// ragged batches and single long sequences balance alike.  The warps of a
+// block take the steps of an item in turn, each with its own softmax state;
+// states are merged through shared memory, and where an item spans several
+// blocks the partial states go to the workspace and the block that finishes
+// last merges them in block order (results do not depend on who is last).
+//
+// The products run on the tensor cores straight from registers, with keys
+// and head dims as the long sides and heads as the short one:
+//   S^T[16 keys][8 heads] = K Q^T,   O^T[16 dims][8 heads] += V^T P^T
+// (mma m16n8k16).  A lane loads 16-byte pieces of K rows (its row, a quarter
+// of each 32 dims) and V rows (its four keys, an eighth of each 64 dims): the
+// order of the dims within the contraction is free, so the pieces are the
+// fragments, and V needs one byte permute per register.  Nothing is staged in
+// shared memory.  tcgen05 would need the rows staged and 128-row tiles with
+// at most 8 useful columns; at 16 flops a byte the kernel is far below the
+// tensor rate either way.
+//
+// The softmax weights enter the value product as a 16-bit value and the
+// 16-bit remainder, so the output keeps the accuracy of 32-bit weights: with
+// up to 4 heads per KV head the remainders ride in the unused columns 4-7
+// (queries duplicated there), above that in a second product.
 #include "mk_ops.cuh"
 
 namespace mk {
 namespace {
 
-constexpr int kPagedWarps = 8;
+constexpr int kMaxBlocksPerSm = 2;
+// steps of a block's range, at least, per warp: see paged_launch
+constexpr int kMinSteps = 4;
 
-template <class T, int D>
-__global__ void __launch_bounds__(kPagedWarps * 32) paged_attn_kernel(PagedArgs a) {
-    constexpr int E = D / 32;   // elements of a head per lane (consecutive)
-    __shared__ float so[kPagedWarps][MK_MAX_GROUP][D];
-    __shared__ float sm[kPagedWarps][MK_MAX_GROUP], sl[kPagedWarps][MK_MAX_GROUP];
-    const int nkv = a.kv.n_kv_heads, G = a.n_q_heads / nkv, ps = a.kv.page_size;
-    const int s = blockIdx.x / nkv, h = blockIdx.x % nkv;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int len = a.lens[s];
-    if (len < 0 || len > a.max_len) {
-        if (threadIdx.x == 0) bad_value(a.status);
-        len = min(max(len, 0), a.max_len);
+__device__ __forceinline__ uint4 ld_stream(const uint16_t *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+template <class T>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    if constexpr (T::kBf16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8x8 transpose of 16-bit elements across the warp
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int D>
+struct PagedShape {
+    static constexpr int kGran = D == 64 ? 2 : 1;    // 16-key groups per step
+    static constexpr int kStep = 16 * kGran;         // keys per step: 8 KB of K and V
+    static constexpr int kWarps = D == 64 ? 8 : 6;
+    static constexpr int kThreads = kWarps * 32;
+};
+
+// Workspace: one counter per block (zero between calls), then two partial
+// states per block: [8 heads][D] sums, [8][2] maxima and sums of weights.
+__host__ __device__ constexpr size_t slot_floats(int d) { return (size_t)MK_MAX_GROUP * d + 2 * MK_MAX_GROUP; }
+__host__ __device__ constexpr size_t counter_bytes(int blocks) { return ((size_t)blocks * 4 + 255) & ~(size_t)255; }
+
+struct PagedParams {
+    PagedArgs a;
+    int max_blocks;      // counters in the workspace
+};
+
+template <class T, int D, bool G4>
+__global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(const __grid_constant__ PagedParams p) {
+    using S = PagedShape<D>;
+    constexpr int NW = S::kWarps, NT = S::kThreads, KG = S::kGran, JK = D / 32, JV = D / 64;
+    __shared__ float so[NW][MK_MAX_GROUP][D];
+    __shared__ float sm[NW][MK_MAX_GROUP], sl[NW][MK_MAX_GROUP];
+    __shared__ int s_last;
+    const PagedArgs &a = p.a;
+    const int nkv = a.kv.n_kv_heads, G = a.n_q_heads / nkv, ps = a.kv.page_size, ns = a.kv.n_seqs;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int P = gridDim.x, blk = blockIdx.x;
+    const float c = a.scale * 1.4426950408889634f;
+    uint32_t *counters = (uint32_t *)a.workspace;
+    float *slots = (float *)((char *)a.workspace + counter_bytes(p.max_blocks));
+
+    auto clamped = [&](int n) { return min(max(n, 0), a.max_len); };
+    auto steps_of = [&](int n) { return (n + S::kStep - 1) / S::kStep; };
+
+    // ---- all items end to end: this block's range of steps
+    long long total = 0;
+    for (int s = lane; s < ns; s += 32) total += steps_of(clamped(a.lens[s]));
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    total *= nkv;
+    long long per = (total + P - 1) / P;
+    if (per < kMinSteps) per = kMinSteps;
+    const long long lo = blk * per, hi = min(total, lo + per);
+
+    // empty sequences get zeros; lengths outside the bounds are reported
+    for (int s = blk; s < ns; s += P) {
+        const int n = a.lens[s];
+        if (n < 0 || n > a.max_len) bad_value(a.status);
+        if (clamped(n) == 0)
+            for (int i = tid; i < a.n_q_heads * D / 8; i += NT)
+                *reinterpret_cast<uint4 *>((uint16_t *)a.out + s * a.out_stride + i * 8) = make_uint4(0, 0, 0, 0);
     }
-    float q[MK_MAX_GROUP][E], o[MK_MAX_GROUP][E], m[MK_MAX_GROUP], l[MK_MAX_GROUP];
-    for (int g = 0; g < MK_MAX_GROUP; ++g) {
-        m[g] = -INFINITY;
-        l[g] = 0.f;
-        for (int e = 0; e < E; ++e) {
-            o[g][e] = 0.f;
-            q[g][e] = 0.f;
+    if (lo >= hi) return;
+
+    // ---- the sequence holding step lo
+    int seq = 0, len = 0;
+    long long seq0 = 0;   // first step of the sequence
+    for (int s0 = 0;; s0 += 32) {
+        const int n = s0 + lane < ns ? clamped(a.lens[s0 + lane]) : 0;
+        const long long mine = (long long)steps_of(n) * nkv;
+        long long sum = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
         }
-        if (g < G)
-            for (int e = 0; e < E; e += 2) {
-                const uint32_t w = *reinterpret_cast<const uint32_t *>((const uint16_t *)a.q + s * a.q_stride +
-                                                                       (long long)(h * G + g) * D + lane * E + e);
-                const float2 f = T::unpack(w);
-                q[g][e] = f.x * a.scale;
-                q[g][e + 1] = f.y * a.scale;
-            }
+        const unsigned hit = __ballot_sync(0xffffffffu, seq0 + sum > lo);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            seq = s0 + src;
+            len = __shfl_sync(0xffffffffu, n, src);
+            seq0 += __shfl_sync(0xffffffffu, sum - mine, src);
+            break;
+        }
+        seq0 += __shfl_sync(0xffffffffu, sum, 31);
     }
-    for (int j = warp; j < len; j += kPagedWarps) {
-        const int page = a.kv.page_table[(long long)s * a.kv.pages_per_seq + j / ps];
-        if (page < 0 || page >= a.kv.num_pages) {
-            if (lane == 0) bad_value(a.status);
-            continue;
-        }
-        const long long at = (((long long)page * nkv + h) * ps + j % ps) * D + lane * E;
-        float k[E], v[E];
-        for (int e = 0; e < E; e += 2) {
-            const float2 fk = T::unpack(*reinterpret_cast<const uint32_t *>((const uint16_t *)a.kv.k + at + e));
-            const float2 fv = T::unpack(*reinterpret_cast<const uint32_t *>((const uint16_t *)a.kv.v + at + e));
-            k[e] = fk.x; k[e + 1] = fk.y;
-            v[e] = fv.x; v[e + 1] = fv.y;
-        }
+
+    long long cur = lo;
+    while (true) {
+        const int steps = steps_of(len);
+        const int h = (int)((cur - seq0) / steps);
+        const long long item0 = seq0 + (long long)h * steps;
+        const int b = (int)(cur - item0), e = (int)(min(hi, item0 + steps) - item0);
+
+        // queries of this KV head: lane (g, t) holds head g's (G4: head g % 4's)
+        // elements [(4 j + t) 8, +8)
+        uint4 q[JK];
+        {
+            const int hq = G4 ? g & 3 : g;
+            const uint16_t *src = (const uint16_t *)a.q + seq * a.q_stride + (long long)(h * G + hq) * D + t * 8;
 #pragma unroll
-        for (int g = 0; g < MK_MAX_GROUP; ++g) {
-            if (g >= G) break;
-            float x = 0.f;
-            for (int e = 0; e < E; ++e) x = fmaf(q[g][e], k[e], x);
-            x = warp_sum(x);
-            const float mn = fmaxf(m[g], x);
-            const float c = mn == -INFINITY ? 1.f : __expf(m[g] - mn), w = x == -INFINITY ? 0.f : __expf(x - mn);
-            m[g] = mn;
-            l[g] = l[g] * c + w;
-            for (int e = 0; e < E; ++e) o[g][e] = o[g][e] * c + w * v[e];
+            for (int j = 0; j < JK; ++j)
+                q[j] = hq < G ? *reinterpret_cast<const uint4 *>(src + j * 32) : make_uint4(0, 0, 0, 0);
         }
-    }
-    for (int g = 0; g < G; ++g) {
-        for (int e = 0; e < E; ++e) so[warp][g][lane * E + e] = o[g][e];
-        if (lane == 0) { sm[warp][g] = m[g]; sl[warp][g] = l[g]; }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < G * D / 2; i += blockDim.x) {
-        const int g = i / (D / 2), e = i % (D / 2) * 2;
-        float M = -INFINITY, L = 0.f, x = 0.f, y = 0.f;
-        for (int w = 0; w < kPagedWarps; ++w) M = fmaxf(M, sm[w][g]);
-        for (int w = 0; w < kPagedWarps; ++w) {
-            const float c = sl[w][g] == 0.f ? 0.f : __expf(sm[w][g] - M);
-            L += c * sl[w][g];
-            x += c * so[w][g][e];
-            y += c * so[w][g][e + 1];
+        float acc[JV * 4][4];
+#pragma unroll
+        for (int i = 0; i < JV * 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // heads 2t, 2t + 1
+
+        const int32_t *table = a.kv.page_table + (long long)seq * a.kv.pages_per_seq;
+        // cache row of this lane's key of a step; -1: not there
+        auto row_of = [&](int i) {
+            const int pos = i * S::kStep + lane % S::kStep;
+            if (i >= e || pos >= len) return -1;
+            const int page = table[pos / ps];
+            if (page < 0 || page >= a.kv.num_pages) {
+                bad_value(a.status);
+                return -1;
+            }
+            return (page * nkv + h) * ps + pos % ps;
+        };
+        uint4 kr[KG][2][JK], vr[KG][4][JV];
+        auto load_k = [&](int row) {
+#pragma unroll
+            for (int r = 0; r < KG; ++r)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int rr = __shfl_sync(0xffffffffu, row, r * 16 + x * 8 + g);
+                    const uint16_t *src = (const uint16_t *)a.kv.k + (long long)rr * D + t * 8;
+#pragma unroll
+                    for (int j = 0; j < JK; ++j)
+                        kr[r][x][j] = rr >= 0 ? ld_stream(src + j * 32) : make_uint4(0, 0, 0, 0);
+                }
+        };
+        auto load_v = [&](int row) {
+#pragma unroll
+            for (int r = 0; r < KG; ++r)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int rr = __shfl_sync(0xffffffffu, row, r * 16 + (x >> 1) * 8 + 2 * t + (x & 1));
+                    const uint16_t *src = (const uint16_t *)a.kv.v + (long long)rr * D + g * 8;
+#pragma unroll
+                    for (int j = 0; j < JV; ++j)
+                        vr[r][x][j] = rr >= 0 ? ld_stream(src + j * 64) : make_uint4(0, 0, 0, 0);
+                }
+        };
+
+        int i = b + warp;
+        int row = row_of(i), next = row_of(i + NW);
+        if (i < e) {
+            load_k(row);
+            load_v(row);
         }
-        const float r = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-        *reinterpret_cast<uint32_t *>((uint16_t *)a.out + s * a.out_stride + (long long)(h * G + g) * D + e) =
-            T::pack(x * r, y * r);
+        for (; i < e; i += NW) {
+            // scores, keys g and g + 8 of each group, heads 2t and 2t + 1
+            float s[KG][4];
+#pragma unroll
+            for (int r = 0; r < KG; ++r) {
+                s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.f;
+#pragma unroll
+                for (int j = 0; j < JK; ++j) {
+                    mma16816<T>(s[r], kr[r][0][j].x, kr[r][1][j].x, kr[r][0][j].y, kr[r][1][j].y, q[j].x, q[j].y);
+                    mma16816<T>(s[r], kr[r][0][j].z, kr[r][1][j].z, kr[r][0][j].w, kr[r][1][j].w, q[j].z, q[j].w);
+                }
+            }
+            const int after = row_of(i + 2 * NW);
+            load_k(next);
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int r = 0; r < KG; ++r)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const bool there = __shfl_sync(0xffffffffu, row, r * 16 + x * 8 + g) >= 0;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        s[r][2 * x + k] = there ? s[r][2 * x + k] * c : -INFINITY;
+                        top[k] = fmaxf(top[k], s[r][2 * x + k]);
+                    }
+                }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                for (int o = 4; o < 32; o <<= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
+            // raise the reference maxima only when one rises by more than 2^8
+            const bool up = top[0] > m[0] + 8.f || top[1] > m[1] + 8.f;
+            if (__any_sync(0xffffffffu, up)) {
+                float f[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float n = fmaxf(m[k], top[k]);
+                    f[k] = n == m[k] ? 1.f : ex2(m[k] - n);
+                    m[k] = n;
+                    l[k] *= f[k];
+                }
+#pragma unroll
+                for (int y = 0; y < JV * 4; ++y)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[y][k] *= f[k & 1];
+            }
+            const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
+#pragma unroll
+            for (int r = 0; r < KG; ++r) {
+                uint32_t hi2[2], lo2[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float w0 = ex2(s[r][2 * x] - m0), w1 = ex2(s[r][2 * x + 1] - m1);
+                    l[0] += w0;
+                    l[1] += w1;
+                    const uint32_t wh = T::pack(w0, w1);
+                    const float2 back = T::unpack(wh);
+                    const uint32_t wl = T::pack(w0 - back.x, w1 - back.y);
+                    if constexpr (G4) hi2[x] = transpose8(t < 2 ? wh : wl);
+                    else {
+                        hi2[x] = transpose8(wh);
+                        lo2[x] = transpose8(wl);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < JV; ++j)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint32_t v0 = word(vr[r][0][j], y), v1 = word(vr[r][1][j], y), v2 = word(vr[r][2][j], y),
+                                       v3 = word(vr[r][3][j], y);
+                        const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632),
+                                       a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
+                        mma16816<T>(acc[j * 4 + y], a0, a1, a2, a3, hi2[0], hi2[1]);
+                        if constexpr (!G4) mma16816<T>(acc[j * 4 + y], a0, a1, a2, a3, lo2[0], lo2[1]);
+                    }
+            }
+            load_v(next);
+            row = next;
+            next = after;
+        }
+
+        // ---- merge the warps' states
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            for (int o = 4; o < 32; o <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
+        if constexpr (G4) {
+#pragma unroll
+            for (int y = 0; y < JV * 4; ++y)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[y][k] += __shfl_xor_sync(0xffffffffu, acc[y][k], 2);
+        }
+        if (!G4 || t < 2) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (g == 0) {
+                    sm[warp][2 * t + k] = m[k];
+                    sl[warp][2 * t + k] = l[k];
+                }
+#pragma unroll
+                for (int j = 0; j < JV; ++j)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        *reinterpret_cast<float2 *>(&so[warp][2 * t + k][(j * 8 + g) * 8 + 2 * y]) =
+                            make_float2(acc[j * 4 + y][k], acc[j * 4 + y][2 + k]);
+            }
+        }
+        __syncthreads();
+        const bool whole = b == 0 && e == steps;
+        // an item's first block keeps its part in slot 1 (its last item), later ones in slot 0
+        float *slot = slots + (size_t)(2 * blk + (b == 0)) * slot_floats(D);
+        for (int idx = tid; idx < G * D / 2; idx += NT) {
+            const int hd = idx / (D / 2), x = idx % (D / 2) * 2;
+            float M = -INFINITY, L = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) M = fmaxf(M, sm[w][hd]);
+            const float M0 = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float f = ex2(sm[w][hd] - M0);   // 0 for a warp that saw nothing
+                L += f * sl[w][hd];
+                o0 += f * so[w][hd][x];
+                o1 += f * so[w][hd][x + 1];
+            }
+            if (whole) {
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+                *reinterpret_cast<uint32_t *>((uint16_t *)a.out + seq * a.out_stride + (long long)(h * G + hd) * D +
+                                              x) = T::pack(o0 * inv, o1 * inv);
+            } else {
+                *reinterpret_cast<float2 *>(slot + hd * D + x) = make_float2(o0, o1);
+                if (x == 0) *reinterpret_cast<float2 *>(slot + MK_MAX_GROUP * D + hd * 2) = make_float2(M, L);
+            }
+        }
+        if (!whole) {
+            // ---- the block that finishes an item last joins its parts
+            const int first = (int)(item0 / per), parts = (int)((item0 + steps - 1) / per) - first + 1;
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) s_last = atomicAdd(&counters[first], 1u) == (uint32_t)parts - 1;
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                if (tid == 0) counters[first] = 0;   // ready for the next call
+                auto part = [&](int i) { return slots + (size_t)(2 * (first + i) + (i == 0)) * slot_floats(D); };
+                // heads' maxima and sums: one warp per head, then every thread its columns
+                float *hm = &sm[0][0], *hl = &sl[0][0];
+                for (int hd = warp; hd < G; hd += NW) {
+                    float M = -INFINITY;
+                    for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(part(i) + MK_MAX_GROUP * D + hd * 2));
+                    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                    const float M0 = M == -INFINITY ? 0.f : M;
+                    float L = 0.f;
+                    for (int i = lane; i < parts; i += 32) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part(i) + MK_MAX_GROUP * D + hd * 2));
+                        L += ex2(ml.x - M0) * ml.y;
+                    }
+                    L = warp_sum(L);
+                    if (lane == 0) { hm[hd] = M0; hl[hd] = L; }
+                }
+                __syncthreads();
+                const int cols = G * D / 4, groups = max(1, NT / cols);
+                float4 *red = reinterpret_cast<float4 *>(&so[0][0][0]);   // [groups][cols]
+                for (int idx = tid; idx < cols * groups; idx += NT) {
+                    const int col = idx % cols, grp = idx / cols, hd = col / (D / 4);
+                    const float M0 = hm[hd];
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int i = grp; i < parts; i += groups) {
+                        const float f = ex2(__ldcg(part(i) + MK_MAX_GROUP * D + hd * 2) - M0);
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(part(i)) + col);
+                        o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+                    }
+                    red[idx] = o;
+                }
+                __syncthreads();
+                for (int col = tid; col < cols; col += NT) {
+                    float4 o = red[col];
+                    for (int grp = 1; grp < groups; ++grp) {
+                        const float4 v = red[grp * cols + col];
+                        o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+                    }
+                    const float L = hl[col / (D / 4)], inv = L == 0.f ? 0.f : 1.f / L;
+                    uint2 w;
+                    w.x = T::pack(o.x * inv, o.y * inv);
+                    w.y = T::pack(o.z * inv, o.w * inv);
+                    *reinterpret_cast<uint2 *>((uint16_t *)a.out + seq * a.out_stride + (long long)h * G * D +
+                                               col * 4) = w;
+                }
+            }
+        }
+        __syncthreads();   // the shared states are free again
+
+        // ---- next item of the range
+        cur = item0 + e;
+        if (cur >= hi) return;
+        while (cur >= seq0 + (long long)steps_of(len) * nkv) {
+            seq0 += (long long)steps_of(len) * nkv;
+            len = clamped(a.lens[++seq]);
+        }
     }
 }
 
 }  // namespace
 
-size_t paged_workspace(const mk_paged_kv &, int, int, int) { return 0; }
+static int max_blocks(int num_sms) { return kMaxBlocksPerSm * num_sms; }
 
-cudaError_t paged_launch(const PagedArgs &a, int, int, cudaStream_t stream) {
-    const int grid = a.kv.n_seqs * a.kv.n_kv_heads;
+static int grid_of(const mk_paged_kv &kv, int max_len, int num_sms) {
+    const int step = kv.head_dim == 64 ? PagedShape<64>::kStep : PagedShape<128>::kStep;
+    const long long most = (long long)kv.n_seqs * kv.n_kv_heads * ((max_len + step - 1) / step);
+    const long long want = (most + kMinSteps - 1) / kMinSteps;
+    return (int)(want < 1 ? 1 : want > max_blocks(num_sms) ? max_blocks(num_sms) : want);
+}
+
+size_t paged_workspace(const mk_paged_kv &kv, int max_len, int, int num_sms) {
+    return counter_bytes(max_blocks(num_sms)) +
+           (size_t)grid_of(kv, max_len, num_sms) * 2 * slot_floats(kv.head_dim) * sizeof(float);
+}
+
+template <class T, int D>
+static void paged_go(const PagedParams &p, int grid, cudaStream_t stream) {
+    if (p.a.n_q_heads / p.a.kv.n_kv_heads <= 4)
+        paged_attn_kernel<T, D, true><<<grid, PagedShape<D>::kThreads, 0, stream>>>(p);
+    else
+        paged_attn_kernel<T, D, false><<<grid, PagedShape<D>::kThreads, 0, stream>>>(p);
+}
+
+cudaError_t paged_launch(const PagedArgs &a, int, int num_sms, cudaStream_t stream) {
+    PagedParams p{a, max_blocks(num_sms)};
+    const int grid = grid_of(a.kv, a.max_len, num_sms);
     if (a.kv.dtype == MK_BF16) {
-        if (a.kv.head_dim == 64) paged_attn_kernel<Bf16, 64><<<grid, kPagedWarps * 32, 0, stream>>>(a);
-        else paged_attn_kernel<Bf16, 128><<<grid, kPagedWarps * 32, 0, stream>>>(a);
+        if (a.kv.head_dim == 64) paged_go<Bf16, 64>(p, grid, stream);
+        else paged_go<Bf16, 128>(p, grid, stream);
     } else {
-        if (a.kv.head_dim == 64) paged_attn_kernel<Fp16, 64><<<grid, kPagedWarps * 32, 0, stream>>>(a);
-        else paged_attn_kernel<Fp16, 128><<<grid, kPagedWarps * 32, 0, stream>>>(a);
+        if (a.kv.head_dim == 64) paged_go<Fp16, 64>(p, grid, stream);
+        else paged_go<Fp16, 128>(p, grid, stream);
     }
     return cudaGetLastError();
 }

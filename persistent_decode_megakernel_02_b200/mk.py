@@ -514,7 +514,7 @@ def paged_attention_workspace(cache: PagedKV, n_q_heads: int, max_len: int):
     with _On(cache.device):
         _check(_lib.mk_paged_attention_workspace(cache._ref, max_len, n_q_heads, C.byref(n)),
                "mk_paged_attention_workspace")
-    return torch.empty(n.value, dtype=torch.uint8, device=cache.device)
+    return torch.zeros(n.value, dtype=torch.uint8, device=cache.device)
 
 
 def paged_attention(cache: PagedKV, q, kv_lens, max_len: int, out, workspace=None, scale=None, status=None,

@@ -21,7 +21,8 @@ def cache(**kw):
 BAD_CACHES = [dict(k=None), dict(v=A + 8), dict(page_table=None), dict(page_table=A + 2), dict(n_seqs=0),
               dict(pages_per_seq=0), dict(num_pages=0), dict(page_size=0), dict(page_size=-1), dict(n_kv_heads=0),
               dict(head_dim=96), dict(head_dim=0), dict(dtype=2), dict(dtype=-1),
-              dict(pages_per_seq=1 << 20, page_size=1 << 20)]
+              dict(pages_per_seq=1 << 20, page_size=1 << 20),
+              dict(num_pages=1 << 26)]
 
 
 def append(c=None, **kw):
