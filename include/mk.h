@@ -586,7 +586,8 @@ int mk_kv_append(const mk_paged_kv *kv, const int32_t *cu_tokens, const int32_t 
  *   kv_lens   device int32 [n_seqs]
  *   max_len   host bound on kv_lens (at most pages_per_seq * page_size): it
  *             sizes the launch and the workspace, so that the same launch can
- *             be replayed while the lengths grow up to it.
+ *             be replayed while the lengths grow up to it.  n_seqs *
+ *             n_kv_heads * (max_len + 512) is below 2^34.
  *   q, out    [n_seqs][n_q_heads][head_dim], the cache's dtype
  *   scale     > 0; usually 1 / sqrt(head_dim)
  *   workspace device, 16-byte aligned, at least the bytes

@@ -127,7 +127,8 @@ int mk_paged_attention(const mk_paged_kv *kv, const int32_t *kv_lens, int max_le
     if (!rows_ok(q, q_stride, qw) || !rows_ok(out, out_stride, qw)) return MK_ERR_INVALID;
     if (!(scale > 0.f) || std::isinf(scale)) return MK_ERR_INVALID;
     if (!aligned_or_null(workspace, 16)) return MK_ERR_INVALID;
-    if ((long long)kv->n_seqs * kv->n_kv_heads > 0x7fffffffLL) return MK_ERR_INVALID;
+    // the work, in steps of 16 positions and their overheads, fits an int
+    if (((double)max_len / 16 + 32) * kv->n_seqs * kv->n_kv_heads > 2147000000.0) return MK_ERR_INVALID;
     int dev, sms;
     const int st = ops_device(&dev, &sms);
     if (st != MK_OK) return st;

@@ -32,8 +32,10 @@ namespace mk {
 namespace {
 
 constexpr int kMaxBlocksPerSm = 2;
-// steps of a block's range, at least, per warp: see paged_launch
-constexpr int kMinSteps = 4;
+// A block's part of an item is at least kMinSteps steps; an item costs a block
+// about kItemCost steps whatever its length (one 128-position item a block:
+// 5.4 us in all, 17 items of 2 steps after one another 30 us).
+constexpr int kMinSteps = 8, kItemCost = 16;
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t *p) {
     uint4 v;
@@ -107,34 +109,60 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
     auto clamped = [&](int n) { return min(max(n, 0), a.max_len); };
     auto steps_of = [&](int n) { return (n + S::kStep - 1) / S::kStep; };
 
-    // ---- all items end to end: this block's range of steps
-    long long total = 0;
-    for (int s = lane; s < ns; s += 32) total += steps_of(clamped(a.lens[s]));
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    // ---- this block's part of the work.  Two rules, by what the lengths give:
+    //  one item per block (`single`): an item is cut into equal parts of at
+    //   most C steps, C such that all parts fit the grid;
+    //  ranges: all items end to end, each with `item_cost` steps ahead of its
+    //   own for what it costs whatever its length, cut into equal ranges.
+    const int n0 = lane < ns ? a.lens[lane] : 0;
+    auto len_of = [&](int s0) { return s0 == 0 ? clamped(n0) : s0 + lane < ns ? clamped(a.lens[s0 + lane]) : 0; };
+    int total = 0, items = 0;
+    for (int s0 = 0; s0 < ns; s0 += 32) {
+        const int n = len_of(s0);
+        total += steps_of(n);
+        items += n > 0;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        items += __shfl_xor_sync(0xffffffffu, items, o);
+    }
+    const int all_items = items * nkv;
     total *= nkv;
-    long long per = (total + P - 1) / P;
-    if (per < kMinSteps) per = kMinSteps;
-    const long long lo = blk * per, hi = min(total, lo + per);
+    const bool single = 2 * all_items <= P;
+    int per, lo, hi;
+    if (single) {
+        per = max((total + P - all_items - 1) / (P - all_items), kMinSteps);
+        lo = blk;
+        hi = P;
+    } else {
+        total += all_items * kItemCost;
+        per = max((total - 1) / P + 1, kMinSteps);
+        lo = min(blk * per, total);   // blk * per < total + P * kMinSteps
+        hi = min(total, lo + per);
+    }
+    auto parts_of = [&](int n) { return (steps_of(n) + per - 1) / per; };   // single
+    auto cost_of = [&](int n) { return n <= 0 ? 0 : single ? parts_of(n) : steps_of(n) + kItemCost; };
 
     // empty sequences get zeros; lengths outside the bounds are reported
-    for (int s = blk; s < ns; s += P) {
-        const int n = a.lens[s];
-        if (n < 0 || n > a.max_len) bad_value(a.status);
-        if (clamped(n) == 0)
-            for (int i = tid; i < a.n_q_heads * D / 8; i += NT)
-                *reinterpret_cast<uint4 *>((uint16_t *)a.out + s * a.out_stride + i * 8) = make_uint4(0, 0, 0, 0);
-    }
-    if (lo >= hi) return;
-
+    auto empties = [&] {
+        for (int s = blk; s < ns; s += P) {
+            const int n = a.lens[s];
+            if (n < 0 || n > a.max_len) bad_value(a.status);
+            if (clamped(n) == 0)
+                for (int i = tid; i < a.n_q_heads * D / 8; i += NT)
+                    *reinterpret_cast<uint4 *>((uint16_t *)a.out + s * a.out_stride + i * 8) = make_uint4(0, 0, 0, 0);
+        }
+    };
     // ---- the sequence holding step lo
     int seq = 0, len = 0;
-    long long seq0 = 0;   // first step of the sequence
-    for (int s0 = 0;; s0 += 32) {
-        const int n = s0 + lane < ns ? clamped(a.lens[s0 + lane]) : 0;
-        const long long mine = (long long)steps_of(n) * nkv;
-        long long sum = mine;
+    int seq0 = 0;   // first step of the sequence
+    bool found = false;
+    for (int s0 = 0; s0 < ns && !found; s0 += 32) {
+        const int n = len_of(s0);
+        const int mine = cost_of(n) * nkv;
+        int sum = mine;
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += y;
         }
         const unsigned hit = __ballot_sync(0xffffffffu, seq0 + sum > lo);
@@ -143,17 +171,36 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
             seq = s0 + src;
             len = __shfl_sync(0xffffffffu, n, src);
             seq0 += __shfl_sync(0xffffffffu, sum - mine, src);
-            break;
-        }
-        seq0 += __shfl_sync(0xffffffffu, sum, 31);
+            found = true;
+        } else
+            seq0 += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (!found) {
+        empties();
+        return;
     }
 
-    long long cur = lo;
+    int cur = lo;
     while (true) {
-        const int steps = steps_of(len);
-        const int h = (int)((cur - seq0) / steps);
-        const long long item0 = seq0 + (long long)h * steps;
-        const int b = (int)(cur - item0), e = (int)(min(hi, item0 + steps) - item0);
+        const int steps = steps_of(len), cost = cost_of(len);
+        const int h = (cur - seq0) / cost;
+        int b, e, first, parts;   // steps [b, e) of the item; its parts are blocks first..
+        if (single) {
+            const int i = cur - seq0 - h * cost;
+            parts = cost;
+            first = blk - i;
+            b = (int)((long long)steps * i / parts);
+            e = (int)((long long)steps * (i + 1) / parts);
+            cur = hi;
+        } else {
+            const int item0 = seq0 + h * cost + kItemCost;   // its first step
+            b = max(cur - item0, 0);
+            e = min(hi, item0 + steps) - item0;
+            first = item0 / per;
+            parts = (item0 + steps - 1) / per - first + 1;
+            cur = item0 + steps;
+        }
+        if (e > b) {
 
         // queries of this KV head: lane (g, t) holds head g's (G4: head g % 4's)
         // elements [(4 j + t) 8, +8)
@@ -349,56 +396,62 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
         }
         if (!whole) {
             // ---- the block that finishes an item last joins its parts
-            const int first = (int)(item0 / per), parts = (int)((item0 + steps - 1) / per) - first + 1;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) s_last = atomicAdd(&counters[first], 1u) == (uint32_t)parts - 1;
+            __syncthreads();   // the block's part is written; the counter's release covers it
+            if (tid == 0) s_last = atom_add_acqrel_gpu(&counters[first], 1u) == (uint32_t)parts - 1;
             __syncthreads();
             if (s_last) {
-                __threadfence();
                 if (tid == 0) counters[first] = 0;   // ready for the next call
                 auto part = [&](int i) { return slots + (size_t)(2 * (first + i) + (i == 0)) * slot_floats(D); };
-                // heads' maxima and sums: one warp per head, then every thread its columns
-                float *hm = &sm[0][0], *hl = &sl[0][0];
-                for (int hd = warp; hd < G; hd += NW) {
-                    float M = -INFINITY;
-                    for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(part(i) + MK_MAX_GROUP * D + hd * 2));
-                    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-                    const float M0 = M == -INFINITY ? 0.f : M;
-                    float L = 0.f;
-                    for (int i = lane; i < parts; i += 32) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part(i) + MK_MAX_GROUP * D + hd * 2));
-                        L += ex2(ml.x - M0) * ml.y;
-                    }
-                    L = warp_sum(L);
-                    if (lane == 0) { hm[hd] = M0; hl[hd] = L; }
-                }
-                __syncthreads();
+                // a thread takes four columns of every groups-th part, with a
+                // running maximum; the groups' results meet in shared memory
                 const int cols = G * D / 4, groups = max(1, NT / cols);
-                float4 *red = reinterpret_cast<float4 *>(&so[0][0][0]);   // [groups][cols]
+                float4 *red = reinterpret_cast<float4 *>(&so[0][0][0]);             // [groups][cols]
+                float2 *ml = reinterpret_cast<float2 *>(&so[0][0][0]) + 2 * NT;      // the same, M and L
                 for (int idx = tid; idx < cols * groups; idx += NT) {
                     const int col = idx % cols, grp = idx / cols, hd = col / (D / 4);
-                    const float M0 = hm[hd];
+                    float M = -INFINITY, L = 0.f;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
                     for (int i = grp; i < parts; i += groups) {
-                        const float f = ex2(__ldcg(part(i) + MK_MAX_GROUP * D + hd * 2) - M0);
+                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(part(i) + MK_MAX_GROUP * D + hd * 2));
                         const float4 v = __ldcg(reinterpret_cast<const float4 *>(part(i)) + col);
-                        o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+                        const float n = fmaxf(M, x.x), N = n == -INFINITY ? 0.f : n;
+                        const float f = ex2(M - N), w = ex2(x.x - N);
+                        M = n;
+                        L = L * f + w * x.y;
+                        o.x = o.x * f + w * v.x;
+                        o.y = o.y * f + w * v.y;
+                        o.z = o.z * f + w * v.z;
+                        o.w = o.w * f + w * v.w;
                     }
                     red[idx] = o;
+                    if (groups > 1) ml[idx] = make_float2(M, L);
+                    else {
+                        const float inv = L == 0.f ? 0.f : 1.f / L;
+                        red[idx] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                    }
                 }
                 __syncthreads();
                 for (int col = tid; col < cols; col += NT) {
                     float4 o = red[col];
-                    for (int grp = 1; grp < groups; ++grp) {
-                        const float4 v = red[grp * cols + col];
-                        o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+                    if (groups > 1) {
+                        float M = -INFINITY, L = 0.f;
+                        for (int grp = 0; grp < groups; ++grp) M = fmaxf(M, ml[grp * cols + col].x);
+                        const float M0 = M == -INFINITY ? 0.f : M;
+                        o = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int grp = 0; grp < groups; ++grp) {
+                            const float4 v = red[grp * cols + col];
+                            const float2 x = ml[grp * cols + col];
+                            const float w = ex2(x.x - M0);
+                            L += w * x.y;
+                            o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+                        }
+                        const float inv = L == 0.f ? 0.f : 1.f / L;
+                        o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
                     }
-                    const float L = hl[col / (D / 4)], inv = L == 0.f ? 0.f : 1.f / L;
                     uint2 w;
-                    w.x = T::pack(o.x * inv, o.y * inv);
-                    w.y = T::pack(o.z * inv, o.w * inv);
+                    w.x = T::pack(o.x, o.y);
+                    w.y = T::pack(o.z, o.w);
                     *reinterpret_cast<uint2 *>((uint16_t *)a.out + seq * a.out_stride + (long long)h * G * D +
                                                col * 4) = w;
                 }
@@ -406,14 +459,15 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
         }
         __syncthreads();   // the shared states are free again
 
+        }
         // ---- next item of the range
-        cur = item0 + e;
-        if (cur >= hi) return;
-        while (cur >= seq0 + (long long)steps_of(len) * nkv) {
-            seq0 += (long long)steps_of(len) * nkv;
+        if (cur >= hi) break;
+        while (cur >= seq0 + cost_of(len) * nkv) {
+            seq0 += cost_of(len) * nkv;
             len = clamped(a.lens[++seq]);
         }
     }
+    empties();
 }
 
 }  // namespace
@@ -422,8 +476,7 @@ static int max_blocks(int num_sms) { return kMaxBlocksPerSm * num_sms; }
 
 static int grid_of(const mk_paged_kv &kv, int max_len, int num_sms) {
     const int step = kv.head_dim == 64 ? PagedShape<64>::kStep : PagedShape<128>::kStep;
-    const long long most = (long long)kv.n_seqs * kv.n_kv_heads * ((max_len + step - 1) / step);
-    const long long want = (most + kMinSteps - 1) / kMinSteps;
+    const long long want = (long long)kv.n_seqs * kv.n_kv_heads * ((max_len + step * kMinSteps - 1) / (step * kMinSteps));
     return (int)(want < 1 ? 1 : want > max_blocks(num_sms) ? max_blocks(num_sms) : want);
 }
 

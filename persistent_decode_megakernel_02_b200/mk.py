@@ -395,58 +395,46 @@ def _dtype_code(dtype) -> int:
     return MK_BF16 if dtype is torch.bfloat16 else MK_FP16 if dtype is torch.float16 else -1
 
 
-def _rows(what: str, name: str, t, dtype, device, rows: int, heads: int, d: int) -> int:
+def _rows(what: str, name: str, t, dtype, dev: int, shape: tuple) -> int:
     """Stride between the tokens of a [rows][heads][d] tensor whose heads are
     contiguous."""
-    if t.dtype is not dtype or t.device != device:
-        _invalid(what, f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != heads or t.shape[2] != d:
-        _invalid(what, f"{name} must be [{rows}][{heads}][{d}], got {list(t.shape)}")
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _invalid(what, f"{name} must be {dtype} {list(shape)} on cuda:{dev}, got {t.dtype} {list(t.shape)} on {t.device}")
     st = t.stride()
-    if rows and (st[2] != 1 or (heads > 1 and st[1] != d)):
+    rows, heads, d = shape
+    if rows <= 1:
+        return heads * d
+    if st[2] != 1 or (st[1] != d and heads > 1):
         _invalid(what, f"{name}'s heads must be contiguous")
-    return st[0] if rows > 1 else max(st[0], heads * d) // 8 * 8
+    return st[0]
 
 
-def _vec(what: str, name: str, t, dtype, device, n: int):
+def _vec(what: str, name: str, t, dtype, dev: int, n: int):
     if t is None:
         return None
-    if t.dtype is not dtype or t.device != device or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        _invalid(what, f"{name} must be a contiguous {dtype} vector of {n} on {device}, "
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        _invalid(what, f"{name} must be a contiguous {dtype} vector of {n} on cuda:{dev}, "
                        f"got {t.dtype} {list(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _status_ptr(what: str, t, device):
+def _launch(what: str, fn, dev: int, stream, args: tuple):
+    """Call `fn(*args, stream)` with device `dev` current, on `stream` or the
+    device's current stream."""
     import torch
-    return _vec(what, "status", t, torch.int32, device, 1)
-
-
-class _On:
-    """Makes a device current for a call when it is not."""
-    __slots__ = ("guard",)
-
-    def __init__(self, device):
-        import torch
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _stream_on(what: str, stream, device):
-    """The raw stream of a call: the given one, or the device's current one."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(device.index) or None
-    if stream.device != device:
-        _invalid(what, f"the stream is on {stream.device}, the tensors on {device}")
-    return int(stream.cuda_stream) or None
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device.index != dev:
+            _invalid(what, f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
+    if st != MK_OK:
+        raise MkError(st, "mk_" + what)
 
 
 class PagedKV:
@@ -466,7 +454,7 @@ class PagedKV:
                 or not page_table.is_contiguous()):
             _invalid(what, "page_table must be a contiguous int32 [n_seqs][pages_per_seq] on k's device")
         self.k, self.v, self.page_table = k, v, page_table
-        self.dtype, self.device = k.dtype, k.device
+        self.dtype, self.device, self.dev = k.dtype, k.device, k.get_device()
         self.n_seqs, self.pages_per_seq = page_table.shape
         self.num_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self._st = PagedKVStruct(_ptr(k), _ptr(v), _ptr(page_table), self.n_seqs, self.pages_per_seq,
@@ -482,36 +470,41 @@ def kv_append(cache: PagedKV, q, k, v, cu_tokens, start_pos, rope_theta: float, 
     start_pos int32 [n_seqs].  q_out (default: in place) receives the rotated
     q, k_out (default: not kept) the rotated k as rows."""
     import torch
-    what, dev, dt, n, d = "kv_append", cache.device, cache.dtype, k.shape[0], cache.head_dim
-    ks = _rows(what, "k", k, dt, dev, n, cache.n_kv_heads, d)
-    vs = _rows(what, "v", v, dt, dev, n, cache.n_kv_heads, d)
+    what, dev, dt, i32 = "kv_append", cache.dev, cache.dtype, torch.int32
+    n = k.shape[0] if k.dim() else 0
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    ks = _rows(what, "k", k, dt, dev, shape)
+    vs = _rows(what, "v", v, dt, dev, shape)
     nq = qs = qos = kos = 0
+    qp = qop = kop = None
     if q is not None:
         nq = q.shape[1] if q.dim() == 3 else 0
-        q_out = q if q_out is None else q_out
-        qs = _rows(what, "q", q, dt, dev, n, nq, d)
-        qos = _rows(what, "q_out", q_out, dt, dev, n, nq, d)
+        qshape = (n, nq, cache.head_dim)
+        qs = qos = _rows(what, "q", q, dt, dev, qshape)
+        qp = qop = q.data_ptr()
+        if q_out is not None:
+            qos = _rows(what, "q_out", q_out, dt, dev, qshape)
+            qop = q_out.data_ptr()
     elif q_out is not None:
         _invalid(what, "q_out without q")
     if k_out is not None:
-        kos = _rows(what, "k_out", k_out, dt, dev, n, cache.n_kv_heads, d)
-    cu = _vec(what, "cu_tokens", cu_tokens, torch.int32, dev, cache.n_seqs + 1)
-    sp = _vec(what, "start_pos", start_pos, torch.int32, dev, cache.n_seqs)
+        kos = _rows(what, "k_out", k_out, dt, dev, shape)
+        kop = k_out.data_ptr()
+    cu = _vec(what, "cu_tokens", cu_tokens, i32, dev, cache.n_seqs + 1)
+    sp = _vec(what, "start_pos", start_pos, i32, dev, cache.n_seqs)
     if n == 0:
         return
-    with _On(dev):
-        _check(_lib.mk_kv_append(cache._ref, cu, sp, n, nq, q.data_ptr() if nq else None, qs, k.data_ptr(), ks,
-                                 v.data_ptr(), vs, rope_theta, q_out.data_ptr() if nq else None, qos,
-                                 k_out.data_ptr() if k_out is not None else None, kos,
-                                 _status_ptr(what, status, dev), _stream_on(what, stream, dev)), "mk_kv_append")
+    _launch(what, _lib.mk_kv_append, dev, stream,
+            (cache._ref, cu, sp, n, nq, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, rope_theta, qop, qos, kop, kos,
+             _vec(what, "status", status, i32, dev, 1)))
 
 
 def paged_attention_workspace(cache: PagedKV, n_q_heads: int, max_len: int):
-    """A workspace for paged_attention calls of these sizes (uint8 CUDA tensor;
-    calls that may overlap on the device need one each)."""
+    """A workspace for paged_attention calls of these sizes (zero-filled uint8
+    CUDA tensor; calls that may overlap on the device need one each)."""
     import torch
     n = C.c_size_t()
-    with _On(cache.device):
+    with torch.cuda.device(cache.dev):
         _check(_lib.mk_paged_attention_workspace(cache._ref, max_len, n_q_heads, C.byref(n)),
                "mk_paged_attention_workspace")
     return torch.zeros(n.value, dtype=torch.uint8, device=cache.device)
@@ -524,25 +517,20 @@ def paged_attention(cache: PagedKV, q, kv_lens, max_len: int, out, workspace=Non
     number); scale defaults to 1 / sqrt(d).  Without a workspace one is
     allocated for the call on its stream."""
     import torch
-    what, dev, dt, d = "paged_attention", cache.device, cache.dtype, cache.head_dim
+    what, dev, dt, i32, d = "paged_attention", cache.dev, cache.dtype, torch.int32, cache.head_dim
     nq = q.shape[1] if q.dim() == 3 else 0
-    qs = _rows(what, "q", q, dt, dev, cache.n_seqs, nq, d)
-    os_ = _rows(what, "out", out, dt, dev, cache.n_seqs, nq, d)
-    lens = _vec(what, "kv_lens", kv_lens, torch.int32, dev, cache.n_seqs)
+    shape = (cache.n_seqs, nq, d)
+    qs = _rows(what, "q", q, dt, dev, shape)
+    os_ = _rows(what, "out", out, dt, dev, shape)
+    lens = _vec(what, "kv_lens", kv_lens, i32, dev, cache.n_seqs)
     if workspace is None:
-        if stream is None:
+        with torch.cuda.stream(stream):     # None: the current stream stays
             workspace = paged_attention_workspace(cache, nq, max_len)
-        else:
-            with torch.cuda.stream(stream):
-                workspace = paged_attention_workspace(cache, nq, max_len)
-    elif workspace.device != dev or not workspace.is_contiguous():
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         _invalid(what, "workspace must be contiguous on the cache's device")
-    with _On(dev):
-        _check(_lib.mk_paged_attention(cache._ref, lens, max_len, nq, q.data_ptr(), qs,
-                                       d ** -0.5 if scale is None else scale, out.data_ptr(), os_,
-                                       workspace.data_ptr() or None, workspace.numel() * workspace.element_size(),
-                                       _status_ptr(what, status, dev), _stream_on(what, stream, dev)),
-               "mk_paged_attention")
+    _launch(what, _lib.mk_paged_attention, dev, stream,
+            (cache._ref, lens, max_len, nq, q.data_ptr(), qs, d ** -0.5 if scale is None else scale, out.data_ptr(),
+             os_, workspace.data_ptr(), workspace.nbytes, _vec(what, "status", status, i32, dev, 1)))
 
 
 def prompt_attention(q, k, v, cu_seqlens, max_len: int, out, scale=None, status=None, stream=None):
@@ -550,24 +538,24 @@ def prompt_attention(q, k, v, cu_seqlens, max_len: int, out, scale=None, status=
     [n][n_q_heads][d], k, v [n][n_kv_heads][d], cu_seqlens int32 [n_seqs + 1],
     max_len a host bound on the lengths; scale defaults to 1 / sqrt(d)."""
     import torch
-    what, dev, dt = "prompt_attention", q.device, q.dtype
-    if q.dim() != 3 or k.dim() != 3 or not q.is_cuda or _dtype_code(dt) < 0:
-        _invalid(what, "q and k must be [n][heads][d] CUDA tensors of bf16 or fp16")
+    what, dev, dt, i32 = "prompt_attention", q.get_device(), q.dtype, torch.int32
+    code = _dtype_code(dt)
+    if q.dim() != 3 or k.dim() != 3 or cu_seqlens.dim() != 1 or dev < 0 or code < 0:
+        _invalid(what, "q and k must be [n][heads][d] CUDA tensors of bf16 or fp16, cu_seqlens a vector")
     n, nq, d = q.shape
-    nkv = k.shape[1]
-    qs = _rows(what, "q", q, dt, dev, n, nq, d)
-    ks = _rows(what, "k", k, dt, dev, n, nkv, d)
-    vs = _rows(what, "v", v, dt, dev, n, nkv, d)
-    os_ = _rows(what, "out", out, dt, dev, n, nq, d)
-    ns = cu_seqlens.shape[0] - 1 if cu_seqlens.dim() == 1 else 0
-    cu = _vec(what, "cu_seqlens", cu_seqlens, torch.int32, dev, ns + 1)
+    nkv, ns = k.shape[1], cu_seqlens.shape[0] - 1
+    kshape = (n, nkv, d)
+    qs = _rows(what, "q", q, dt, dev, (n, nq, d))
+    ks = _rows(what, "k", k, dt, dev, kshape)
+    vs = _rows(what, "v", v, dt, dev, kshape)
+    os_ = _rows(what, "out", out, dt, dev, (n, nq, d))
+    cu = _vec(what, "cu_seqlens", cu_seqlens, i32, dev, ns + 1)
     if n == 0:
         return
-    with _On(dev):
-        _check(_lib.mk_prompt_attention(_dtype_code(dt), nq, nkv, d, cu, ns, n, max_len, q.data_ptr(), qs,
-                                        k.data_ptr(), ks, v.data_ptr(), vs, d ** -0.5 if scale is None else scale,
-                                        out.data_ptr(), os_, _status_ptr(what, status, dev),
-                                        _stream_on(what, stream, dev)), "mk_prompt_attention")
+    _launch(what, _lib.mk_prompt_attention, dev, stream,
+            (code, nq, nkv, d, cu, ns, n, max_len, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+             d ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+             _vec(what, "status", status, i32, dev, 1)))
 
 
 def sample(logits, uniform, token_out, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
@@ -575,17 +563,16 @@ def sample(logits, uniform, token_out, temperature=None, top_k=None, top_p=None,
     be strided) from the given uniform numbers; the parameters are vectors of
     one value per row, or None (temperature 1, filter off)."""
     import torch
-    what, dev = "sample", logits.device
-    if logits.dim() != 2 or logits.dtype is not torch.float32 or not logits.is_cuda or \
-            (logits.shape[1] > 1 and logits.stride(1) != 1):
-        _invalid(what, "logits must be a float32 CUDA tensor [rows][vocab] with contiguous rows")
+    what, dev, f, i = "sample", logits.get_device(), torch.float32, torch.int32
+    if logits.dim() != 2 or logits.dtype is not f or dev < 0:
+        _invalid(what, "logits must be a float32 CUDA tensor [rows][vocab]")
     rows, vocab = logits.shape
-    f, i = torch.float32, torch.int32
-    args = (_vec(what, "uniform", uniform, f, dev, rows), _vec(what, "temperature", temperature, f, dev, rows),
+    st = logits.stride()
+    if vocab > 1 and st[1] != 1:
+        _invalid(what, "rows of logits must be contiguous")
+    args = (logits.data_ptr(), st[0] if rows > 1 else vocab, rows, vocab,
+            _vec(what, "uniform", uniform, f, dev, rows), _vec(what, "temperature", temperature, f, dev, rows),
             _vec(what, "top_k", top_k, i, dev, rows), _vec(what, "top_p", top_p, f, dev, rows),
             _vec(what, "min_p", min_p, f, dev, rows), _vec(what, "token_out", token_out, i, dev, rows))
-    if rows == 0:
-        return
-    with _On(dev):
-        _check(_lib.mk_sample(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, rows, vocab, *args,
-                              _stream_on(what, stream, dev)), "mk_sample")
+    if rows:
+        _launch(what, _lib.mk_sample, dev, stream, args)
