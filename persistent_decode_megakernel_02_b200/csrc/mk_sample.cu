@@ -5,15 +5,21 @@
 // in units of 2^-43 of the largest, which makes every sum exact and
 // independent of its order (and of how a row is spread over blocks).
 //
-// A row goes to a cluster of 1 to 8 blocks, which hold it in
-// shared memory from its one read to the end; the blocks exchange maxima, histograms and
-// sums through each other's shared memory.  A row without top-k and top-p is
-// one exchange of sums.  Top-k and top-p first find, by a histogram over the
-// distance from the largest logit (64 bins per unit of l / T), the bin that
-// holds the cut; when at most 512 candidates lie above its lower edge they are
-// gathered in one block, which ranks them pairwise and finishes alone.
-// Otherwise (flat rows, very large k) the cut is found exactly by histograms
-// over a shrinking key range (32 -> 21 -> 10 -> 0 bits left).  No sort.
+// A row goes to a cluster of 1 to 8 blocks, which hold it in shared memory
+// from its one read to the end and exchange maxima, histograms and sums
+// through each other's shared memory.  No sort:
+//  - temperature and min-p alone: one exchange of sums, then the block, vector
+//    step, warp, lane and element that hold uniform * total;
+//  - top-k up to 384: the k-th largest of the threads' maxima is a lower bound
+//    of the k-th largest logit that leaves few logits above it (about k /
+//    (1 - k / 8192) of a row); those are gathered in block 0, which ranks them
+//    pairwise and applies top-p and min-p to them alone;
+//  - top-p alone: a histogram of masses over the distance from the largest
+//    logit (128 bins per unit of l / T) gives the bin that holds the cut; its
+//    logits are gathered and ranked, and the cut goes back to all blocks;
+//  - what these leave over (larger k, many equal logits, very flat rows): the
+//    exact cut by histograms over a shrinking key range (32 -> 21 -> 10 -> 0
+//    bits left).
 //
 // Rows beyond 8 blocks' shared memory take one block each that rereads them.
 #include <atomic>
@@ -39,22 +45,67 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
+// Weights of a row.  2^(y / 32) for y = 32 (x - top) / (T ln 2) <= 0, as 2^n
+// 2^(i / 32) 2^(r / 32): i from a table of 32, and |r| <= 1/2 by the Taylor
+// polynomial of degree 4 (relative error (ln 2 / 64)^5 / 120 < 1.3e-12).  Ten
+// 64-bit operations; the library's exp() made the passes that weigh a whole
+// row twice as long.
+constexpr double kMagic = 6755399441055744.0;     // 1.5 * 2^52: adding it rounds to an integer
+constexpr double kTwo52 = 4503599627370496.0;
+constexpr double kUnit = 8796093022208.0;         // 2^43
+constexpr double kC = 0.021660849392498290;       // ln 2 / 32
 struct Weight {
-    double inv_t;
-    float top;      // the row's largest logit
-    double min_w;   // min-p: weights below it are dropped from the final choice
-    // w = exp((x - top) / T); x is neither NaN nor -infinity
-    __device__ __forceinline__ double real(float x) const {
-        return x == top ? 1.0 : exp(((double)x - (double)top) * inv_t);
-    }
-    __device__ __forceinline__ u64 whole(double w) const { return (u64)(w * 8796093022208.0); }   // 2^43
-    __device__ __forceinline__ void init(const SampleArgs &a, int row, uint32_t top_key, float t) {
-        inv_t = 1.0 / (double)t;
-        top = key_logit(top_key);
+    double c32, off, min_v;      // y = c32 x - off; min_v: min-p, in units
+    float top, reach, floor;     // logits below `reach` weigh nothing, below `floor` nothing in the final choice
+    const double *table;         // 2^(i / 32), shared memory
+
+    __device__ __forceinline__ void init(const SampleArgs &a, int row, float top_, float t, const double *tab) {
+        c32 = 46.166241308446828384 / (double)t;  // 32 / ln 2
+        top = top_;
+        off = (double)top * c32;
+        float far = 31.2f;       // e^-31.2 < 2^-45
         const float mp = a.min_p ? a.min_p[row] : 0.f;
-        min_w = mp > 0.f ? fmin((double)mp, 1.0) : 0.0;
+        min_v = 0.0;
+        if (mp > 0.f) {
+            min_v = fmin((double)mp, 1.0) * kUnit;
+            far = fminf(far, fmaxf(-logf(mp), 0.f) * 1.0001f + 1e-4f);
+        }
+        reach = top - 31.2f * t;
+        floor = top - far * t;
+        table = tab;
+    }
+    // 2^43 w, before rounding; 0 below half a unit, and for -infinity.  No
+    // branches: four of these run side by side in every pass.
+    __device__ __forceinline__ double scaled(float x) const {
+        const double y = fma((double)x, c32, -off);
+        const double shifted = y + kMagic;
+        const int n = __double2loint(shifted);
+        const double d = y - (shifted - kMagic);
+        double e = fma(d, kC * kC * kC * kC / 24, kC * kC * kC / 6);
+        e = fma(d, e, kC * kC / 2);
+        e = fma(d, e, kC);
+        e = fma(d, e, 1.0);
+        const double w = table[n & 31] * e;
+        const double v = __hiloint2double(__double2hiint(w) + (((n >> 5) + 43) << 20), __double2loint(w));
+        return x == top ? kUnit : x >= reach && x > -INFINITY ? v : 0.0;
+    }
+    __device__ __forceinline__ u64 units(double v) const {      // v <= 2^43
+        return (u64)__double_as_longlong(v + kTwo52) & 0xfffffffffffffull;
+    }
+    __device__ __forceinline__ u64 whole(float x) const { return units(scaled(x)); }
+    __device__ __forceinline__ bool enough(float x) const { return scaled(x) >= min_v; }
+    // the weight in the final choice
+    __device__ __forceinline__ u64 final_whole(float x) const {
+        const double v = scaled(x);
+        return v >= min_v ? units(v) : 0;
     }
 };
+__device__ __forceinline__ void fill_table(double *table) {
+    if (threadIdx.x < 32) table[threadIdx.x] = exp2((double)threadIdx.x / 32);
+}
+__device__ __forceinline__ u64 goal_of(float u, u64 total) {
+    return min((u64)((double)(u > 0.f ? fminf(u, 1.f) : 0.f) * (double)total), total - 1);
+}
 
 template <class V>
 __device__ __forceinline__ V block_sum(V v, V *tmp) {
@@ -90,6 +141,7 @@ struct SampShared {
     uint32_t cnt[kBins];
     u64 tmp64[kSampWarps];
     uint32_t tmp32[kSampWarps];
+    double table[32];
     uint32_t bin;
     u64 mass_before, mass_bin;
     uint32_t cnt_before, cnt_bin;
@@ -101,6 +153,7 @@ __global__ void __launch_bounds__(kSampThreads) sample_long_kernel(SampleArgs a)
     const float *x = a.logits + (long long)row * a.stride;
     const int V = a.vocab;
 
+    fill_table(sh.table);
     // largest logit, lowest index first
     u64 best = 0;
     for (int i = tid; i < V; i += kSampThreads) {
@@ -123,7 +176,7 @@ __global__ void __launch_bounds__(kSampThreads) sample_long_kernel(SampleArgs a)
     }
     const uint32_t top_key = (uint32_t)(best >> 32);
     Weight wt;
-    wt.init(a, row, top_key, t);
+    wt.init(a, row, key_logit(top_key), t, sh.table);
     const bool inf_top = isinf(wt.top);
     // an infinite top leaves only its equals
     uint32_t cut = inf_top ? top_key : 1u;    // keys below are out
@@ -140,11 +193,11 @@ __global__ void __launch_bounds__(kSampThreads) sample_long_kernel(SampleArgs a)
             uint32_t eq = 0;
             for (int i = tid; i < V; i += kSampThreads) {
                 const uint32_t key = logit_key(x[i]);
-                if (key > cut) m += wt.whole(wt.real(x[i]));
+                if (key > cut) m += wt.whole(x[i]);
                 eq += key == cut;
             }
             const uint32_t n_eq = block_sum(eq, sh.tmp32);
-            const u64 total = block_sum(m, sh.tmp64) + (u64)min(n_eq, ties) * wt.whole(wt.real(key_logit(cut)));
+            const u64 total = block_sum(m, sh.tmp64) + (cut > 1u ? (u64)min(n_eq, ties) * wt.whole(key_logit(cut)) : 0);
             target = (double)p * (double)total;
         }
         uint32_t lo = cut, hi = top_key;
@@ -161,7 +214,7 @@ __global__ void __launch_bounds__(kSampThreads) sample_long_kernel(SampleArgs a)
                 if (key < lo || key > hi) continue;
                 const uint32_t b = (hi - key) >> sh_bits;
                 atomicAdd(&sh.cnt[b], 1u);
-                if (by_mass) atomicAdd(&sh.mass[b], wt.whole(wt.real(x[i])));
+                if (by_mass) atomicAdd(&sh.mass[b], wt.whole(x[i]));
             }
             __syncthreads();
             // the first bin (from the top) at which the running total reaches the target
@@ -193,7 +246,7 @@ __global__ void __launch_bounds__(kSampThreads) sample_long_kernel(SampleArgs a)
             if (lo == hi) {
                 uint32_t need;
                 if (by_mass) {
-                    const double w = (double)wt.whole(wt.real(key_logit(lo)));
+                    const double w = (double)wt.whole(key_logit(lo));
                     const double n = w > 0 ? ceil((target - (double)mass_above) / w) : 1.0;
                     need = n < 1.0 ? 1u : n > 4e9 ? 0xffffffffu : (uint32_t)n;
                 } else
@@ -210,16 +263,12 @@ __global__ void __launch_bounds__(kSampThreads) sample_long_kernel(SampleArgs a)
     // final choice: warps own consecutive chunks of the row
     const int chunk = ((V + kSampWarps - 1) / kSampWarps + 31) & ~31;
     const int b = min(warp * chunk, V), e = min(b + chunk, V);
-    const double w_cut = cut > 1u ? wt.real(key_logit(cut)) : 0.0;
-    const u64 u_cut = w_cut >= wt.min_w ? wt.whole(w_cut) : 0;
+    const u64 u_cut = cut > 1u ? wt.final_whole(key_logit(cut)) : 0;
     u64 strict = 0;
     uint32_t eq = 0;
     for (int i = b + lane; i < e; i += 32) {
         const uint32_t key = logit_key(x[i]);
-        if (key > cut) {
-            const double w = wt.real(x[i]);
-            if (w >= wt.min_w) strict += wt.whole(w);
-        }
+        if (key > cut) strict += wt.final_whole(x[i]);
         eq += key == cut;
     }
     for (int o = 16; o > 0; o >>= 1) {
@@ -237,9 +286,7 @@ __global__ void __launch_bounds__(kSampThreads) sample_long_kernel(SampleArgs a)
         eq_seen += sh.tmp32[w];
     }
     const u64 mine = strict + (u64)min(ties - min(ties, eq_before), eq) * u_cut;
-    const float u = a.uniform[row];
-    u64 goal = (u64)((double)(u > 0.f ? fminf(u, 1.f) : 0.f) * (double)total);
-    goal = min(goal, total - 1);
+    const u64 goal = goal_of(a.uniform[row], total);
     if (goal < before || goal >= before + mine) return;
     u64 run = before;
     uint32_t tie_rank = eq_before;
@@ -248,10 +295,8 @@ __global__ void __launch_bounds__(kSampThreads) sample_long_kernel(SampleArgs a)
         u64 w = 0;
         const uint32_t key = i < e ? logit_key(x[i]) : 0;
         const unsigned eqm = __ballot_sync(0xffffffffu, key == cut);
-        if (key > cut) {
-            const double f = wt.real(x[i]);
-            if (f >= wt.min_w) w = wt.whole(f);
-        } else if (key == cut && tie_rank + __popc(eqm & ((1u << lane) - 1)) < ties)
+        if (key > cut) w = wt.final_whole(x[i]);
+        else if (key == cut && tie_rank + __popc(eqm & ((1u << lane) - 1)) < ties)
             w = u_cut;
         u64 s = w;
         for (int o = 1; o < 32; o <<= 1) {
@@ -272,30 +317,49 @@ __global__ void __launch_bounds__(kSampThreads) sample_long_kernel(SampleArgs a)
 
 namespace cg = cooperative_groups;
 
-constexpr int kRegThreads = 512, kRegWarps = kRegThreads / 32, kMaxCluster = 8, kListMax = 512;
+constexpr int kRegThreads = 512, kRegWarps = kRegThreads / 32, kMaxCluster = 8;
+constexpr int kListMax = 512;                  // gathered logits, at most
+constexpr int kMaxK = 384;                     // top-k by the threads' maxima, at most
 constexpr int kVecStep = 4 * kRegThreads;      // logits of one vector step of a block
 constexpr int kMaxIt = 22;                     // vector steps of a slice: 176 KB of logits
 
 struct RegShared {
-    u64 mass[kBins];
-    uint32_t cnt[kBins];
-    u64 list_w[kListMax], list_keep[kListMax];
-    uint32_t list_key[kListMax];
-    int32_t list_idx[kListMax];
-    u64 sub[kMaxIt * kRegWarps];          // sums per (vector step, warp)
+    union {
+        struct {
+            u64 mass[kBins];
+            uint32_t cnt[kBins];
+        };
+        uint32_t part[3][kBins];      // masses in three parts of 15, 14 and 14 bits
+        float maxima[kMaxCluster * kRegThreads];
+    };
+    uint32_t bins[kBins];
+    u64 list[kListMax];               // gathered logits: key, then lowest index first
+    u64 sorted[kListMax];
+    u64 sub[kRegWarps];
+    double table[32];
     // written by every block of the cluster, read by all
     u64 x_best[kMaxCluster], x_sum[kMaxCluster], x_mass[kMaxCluster];
     uint32_t x_cnt[kMaxCluster];
     u64 found_mass;
     uint32_t found_bin, found_before, found_cnt;
-    int32_t tie_last;
+    float top, bound, cut;
+    int32_t last;
     uint32_t list_n;
     u64 tmp64[kRegWarps];
     uint32_t tmp32[kRegWarps];
     u64 goal;
-    int hit;
 };
 
+template <class V>
+__device__ __forceinline__ V block_max(V v, V *tmp) {
+    for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kRegWarps; ++w) v = max(v, tmp[w]);
+    return v;
+}
 template <class V>
 __device__ __forceinline__ V reg_block_sum(V v, V *tmp) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -308,28 +372,74 @@ __device__ __forceinline__ V reg_block_sum(V v, V *tmp) {
     return s;
 }
 
-// A block's slice of the row is IT vector steps of 4 logits a thread, kept as
-// keys: vector (it, thread) holds logits 4 (it * 512 + thread).. of the slice,
-// so index order is (it, warp, lane, element).  A thread only ever reads the
-// keys it wrote.
-__global__ void __launch_bounds__(kRegThreads) sample_kernel(SampleArgs a, int IT) {
-    extern __shared__ uint4 keys[];
-    __shared__ RegShared sh;
+// Sort n <= 512 values of shared memory, descending, into `out`: each is
+// counted against all (several threads a value where n leaves them) and put
+// in its place.  Values are distinct.  (A bitonic sort of 64-bit values took
+// twice as long at 20 to 200 of them: its steps are short and dependent.)
+template <class V>
+__device__ __forceinline__ void sort_descending(const V *in, V *out, int n) {
+    const int per = n <= 64 ? 8 : n <= 128 ? 4 : n <= 256 ? 2 : 1;
+    const int i = threadIdx.x / per;
+    if ((threadIdx.x & ~31) / per < n) {       // warps without a value skip the count
+        const V v = in[min(i, n - 1)];
+        int place = 0;
+#pragma unroll 8
+        for (int j = threadIdx.x & (per - 1); j < n; j += per) place += in[j] > v;
+        for (int o = per >> 1; o > 0; o >>= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+        if (i < n && (threadIdx.x & (per - 1)) == 0) out[place] = v;
+    }
+    __syncthreads();
+}
+// Exclusive prefix sum over the block, and the total.
+__device__ __forceinline__ u64 reg_block_scan(u64 v, u64 *tmp, u64 &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    u64 x = v;
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) tmp[warp] = x;
+    __syncthreads();
+    u64 before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kRegWarps; ++w) {
+        if (w == warp) before = all;
+        all += tmp[w];
+    }
+    total = all;
+    return before + x - v;
+}
+
+// A block's slice of the row is 16 warps' parts of IT vector steps (4 logits a
+// lane), so index order is (warp, step, lane, element).  A thread only ever
+// reads the logits it stored; NaN is stored as -infinity.
+__global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, int IT) {
+    extern __shared__ float4 xs[];
+    __shared__ __align__(16) RegShared sh;
     cg::cluster_group cl = cg::this_cluster();
     const int CL = cl.num_blocks(), rank = cl.block_rank();
     const int row = blockIdx.x / CL, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float *x = a.logits + (long long)row * a.stride;
     const int V = a.vocab;
+    RegShared *home = cl.map_shared_rank(&sh, 0);
 
-    // ---- the slice, as keys; 0 beyond the row.  Vectors start at the 16-byte
-    // boundary at or before the row (`skew` logits before it).
+    fill_table(sh.table);
+    if (tid == 0) sh.list_n = 0;
+    const float t = a.temperature ? a.temperature[row] : 1.f;
+    const int k = a.top_k ? a.top_k[row] : 0;
+    const float p = a.top_p ? a.top_p[row] : 1.f;
+
+    // ---- the slice.  Vectors start at the 16-byte boundary at or before the
+    // row (`skew` logits before it).
     const int skew = (int)(((uintptr_t)x >> 2) & 3);
-    const int base = rank * IT * kVecStep - skew;       // index of the slice's first logit
-    u64 best = 0;      // the largest key, lowest index first
-#pragma unroll 4
+    const int base = rank * IT * kVecStep + warp * IT * 128 + lane * 4 - skew;    // the thread's first logit
+    float best = -INFINITY;
+    int best_it = 0;
+#pragma unroll 8
     for (int it = 0; it < IT; ++it) {
-        const int i = base + it * kVecStep + 4 * tid;
-        float4 f = make_float4(NAN, NAN, NAN, NAN);
+        const int i = base + it * 128;
+        float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         if (i >= 0 && i + 4 <= V) f = __ldcs(reinterpret_cast<const float4 *>(x + i));
         else {
             if (i >= 0 && i < V) f.x = x[i];
@@ -337,85 +447,180 @@ __global__ void __launch_bounds__(kRegThreads) sample_kernel(SampleArgs a, int I
             if (i + 2 >= 0 && i + 2 < V) f.z = x[i + 2];
             if (i + 3 >= 0 && i + 3 < V) f.w = x[i + 3];
         }
-        uint4 q;
-        q.x = logit_key(f.x);
-        q.y = logit_key(f.y);
-        q.z = logit_key(f.z);
-        q.w = logit_key(f.w);
-        keys[it * kRegThreads + tid] = q;
-        const uint32_t m = max(max(q.x, q.y), max(q.z, q.w));
-        if (m > (uint32_t)(best >> 32)) {
-            const int c = q.x == m ? 0 : q.y == m ? 1 : q.z == m ? 2 : 3;
-            best = (u64)m << 32 | (uint32_t)~(i + c);
+        f.x = fmaxf(f.x, -INFINITY);      // the other operand where one is NaN
+        f.y = fmaxf(f.y, -INFINITY);
+        f.z = fmaxf(f.z, -INFINITY);
+        f.w = fmaxf(f.w, -INFINITY);
+        xs[it * kRegThreads + tid] = f;
+        const float m = fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w));
+        if (m > best) {
+            best = m;
+            best_it = it;
         }
     }
-    // f(key, index) for every logit of the thread
+    // f(logit, index) for every logit of the thread
     auto each = [&](auto f) {
-#pragma unroll 1
+#pragma unroll 2
         for (int it = 0; it < IT; ++it) {
-            const uint4 q = keys[it * kRegThreads + tid];
-            const int i = base + it * kVecStep + 4 * tid;
+            const float4 q = xs[it * kRegThreads + tid];
+            const int i = base + it * 128;
             f(q.x, i);
             f(q.y, i + 1);
             f(q.z, i + 2);
             f(q.w, i + 3);
         }
     };
-    const float t = a.temperature ? a.temperature[row] : 1.f;
-    const int k = a.top_k ? a.top_k[row] : 0;
-    const float p = a.top_p ? a.top_p[row] : 1.f;
+    auto gather = [&](float f, int i) {
+        const uint32_t at = atomicAdd(&home->list_n, 1u);
+        if (at < kListMax) home->list[at] = (u64)logit_key(f) << 32 | (uint32_t)~i;
+    };
+    auto logit_of = [](u64 id) { return key_logit((uint32_t)(id >> 32)); };
 
-    // ---- the row's largest
-    for (int o = 16; o > 0; o >>= 1) {
-        const u64 c = __shfl_xor_sync(0xffffffffu, best, o);
-        best = c > best ? c : best;
-    }
-    if (lane == 0) sh.tmp64[warp] = best;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kRegWarps; ++w) best = sh.tmp64[w] > best ? sh.tmp64[w] : best;
-    if (tid < CL) cl.map_shared_rank(&sh, tid)->x_best[rank] = best;
-    if (tid == 0) sh.list_n = 0;
-    cl.sync();
-    for (int r = 0; r < CL; ++r) best = sh.x_best[r] > best ? sh.x_best[r] : best;
-    if (best == 0 || !(t > 0.f)) {
-        if (rank == 0 && tid == 0) a.token[row] = best == 0 ? -1 : (int)~(uint32_t)best;
-        return;      // the same for every block; nobody reads another's memory any more
-    }
-    const uint32_t top_key = (uint32_t)(best >> 32);
     Weight wt;
-    wt.init(a, row, top_key, t);
-    uint32_t cut = isinf(wt.top) ? top_key : 1u;   // keys below are out
-    uint32_t ties = 0xffffffffu;                   // of keys equal to cut, this many (lowest indices) stay
     const bool by_k = k > 0 && k < V, by_p = p < 1.f;
+    float top;
+
+    if (by_k && k <= kMaxK && t > 0.f) {
+        // ---- top-k by the threads' maxima
+        home->maxima[rank * kRegThreads + tid] = best;
+        cl.sync();
+        if (rank == 0) {
+            float mk[kMaxCluster], m = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                mk[r] = r < CL ? sh.maxima[r * kRegThreads + tid] : -INFINITY;
+                m = fmaxf(m, mk[r]);
+            }
+            m = block_max(m, reinterpret_cast<float *>(sh.tmp64));
+            for (int i = tid; i < kBins; i += kRegThreads) sh.bins[i] = 0;
+            if (tid == 0) sh.found_bin = 0xffffffffu;
+            __syncthreads();
+            const float scale = fminf(64.f / t, 1e30f);
+            auto bin_of = [&](float f) { return f == m ? 0 : (int)fminf((m - f) * scale, (float)(kBins - 1)); };
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                if (mk[r] > -INFINITY) atomicAdd(&sh.bins[bin_of(mk[r])], 1u);
+            __syncthreads();
+            const uint4 c = reinterpret_cast<const uint4 *>(sh.bins)[tid];
+            uint32_t s = c.x + c.y + c.z + c.w, run = s;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += y;
+            }
+            if (lane == 31) sh.tmp32[warp] = run;
+            __syncthreads();
+            run -= s;
+#pragma unroll
+            for (int w = 0; w < kRegWarps; ++w) run += w < warp ? sh.tmp32[w] : 0;
+            if (run < (uint32_t)k && run + s >= (uint32_t)k) {
+                int b = 0;
+                uint32_t y = run + c.x;
+                if (y < (uint32_t)k) { b = 1; y += c.y; }
+                if (y < (uint32_t)k) { b = 2; y += c.z; }
+                if (y < (uint32_t)k) b = 3;
+                sh.found_bin = 4 * tid + b;
+            }
+            __syncthreads();
+            // the smallest maximum of the bins up to it: at least k logits are no smaller
+            const uint32_t edge = sh.found_bin;
+            float low = INFINITY;
+            if (edge != 0xffffffffu)
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r)
+                    if (mk[r] > -INFINITY && bin_of(mk[r]) <= (int)edge) low = fminf(low, mk[r]);
+            low = -block_max(-low, reinterpret_cast<float *>(sh.tmp64));
+            if (tid < CL) {
+                RegShared *o = cl.map_shared_rank(&sh, tid);
+                o->top = m;
+                o->bound = edge != 0xffffffffu ? low : -INFINITY;
+            }
+        }
+        cl.sync();
+        top = sh.top;
+        const float bound = sh.bound;
+        if (top == -INFINITY) {
+            if (rank == 0 && tid == 0) a.token[row] = -1;
+            return;
+        }
+        wt.init(a, row, top, t, sh.table);
+        if (bound > -INFINITY && top < INFINITY) {
+            each([&](float f, int i) {
+                if (f >= bound) gather(f, i);
+            });
+            cl.sync();
+            const uint32_t n = home->list_n;
+            if (n <= kListMax) {
+                if (rank != 0) return;
+                sort_descending(sh.list, sh.sorted, (int)n);
+                u64 id = tid < n ? sh.sorted[tid] : 0, total;
+                u64 w = tid < n && tid < k ? wt.whole(logit_of(id)) : 0;
+                const u64 before = reg_block_scan(w, sh.tmp64, total);
+                if (by_p && tid > 0 && !((double)before < (double)p * (double)total)) w = 0;
+                if (wt.min_v > 0.0 && w > 0 && !wt.enough(logit_of(id))) w = 0;
+                // in index order, the dropped ones with weight 0
+                if (tid < n) sh.list[tid] = id << 32 | (w ? id >> 32 : 0);
+                __syncthreads();
+                sort_descending(sh.list, sh.sorted, (int)n);
+                id = tid < n ? sh.sorted[tid] : 0;
+                w = (uint32_t)id ? wt.whole(key_logit((uint32_t)id)) : 0;
+                const u64 run = reg_block_scan(w, sh.tmp64, total), goal = goal_of(a.uniform[row], total);
+                if (goal >= run && goal < run + w) a.token[row] = (int)~(uint32_t)(id >> 32);
+                cl.sync();      // the others have read the count (or are gone)
+                return;
+            }
+        }
+    } else {
+        // ---- the row's largest, lowest index first
+        u64 id = 0;
+        if (best > -INFINITY) {
+            const float4 q = xs[best_it * kRegThreads + tid];
+            const int c = q.x == best ? 0 : q.y == best ? 1 : q.z == best ? 2 : 3;
+            id = (u64)logit_key(best) << 32 | (uint32_t)~(base + best_it * 128 + c);
+        }
+        id = block_max(id, sh.tmp64);
+        if (tid < CL) cl.map_shared_rank(&sh, tid)->x_best[rank] = id;
+        cl.sync();
+        for (int r = 0; r < CL; ++r) id = max(id, sh.x_best[r]);
+        if (id == 0 || !(t > 0.f)) {
+            if (rank == 0 && tid == 0) a.token[row] = id == 0 ? -1 : (int)~(uint32_t)id;
+            return;      // the same for every block; nobody reads another's memory any more
+        }
+        top = logit_of(id);
+        wt.init(a, row, top, t, sh.table);
+    }
+
+    // Kept so far: logits above `cut`, and those equal to it up to index
+    // `last`.  An infinite top leaves only its equals.
+    float cut = top == INFINITY ? INFINITY : -INFINITY;
+    int32_t last = 0x7fffffff;
 
     // The histogram bins of all blocks (filled, not yet synchronised): the
-    // first bin at which the running (count, mass) reaches the target, with
-    // what lies before it.  False if none does.  *all_mass: everything's mass.
-    auto find_bin = [&](auto reached, bool masses, uint32_t cnt0, u64 mass0, u64 *all_mass) {
+    // first bin at which reached(count, mass, all mass) turns true over the
+    // running totals, with what lies before it, in sh.found_*.  False if none.
+    auto find_bin = [&](auto reached, bool masses, uint32_t cnt0, u64 mass0) {
         cl.sync();
-        // every block adds up its share of the bins
-        const int share = kBins / CL, lo = rank * share;
+        // every block adds up its share of the bins, consecutive ones per thread
+        const int share = kBins / CL, lo = rank * share, per = max(share / kRegThreads, 1);
         if (tid == 0) sh.found_bin = 0xffffffffu;
-        uint32_t c[4] = {0, 0, 0, 0};      // consecutive bins per thread: share <= 4 * 512
+        uint32_t c[4] = {0, 0, 0, 0};
         u64 m[4] = {0, 0, 0, 0};
-        const int per = (share + kRegThreads - 1) / kRegThreads;
         uint32_t csum = 0;
         u64 msum = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int b = tid * per + i;
             if (i < per && b < share) {
-                for (int r = 0; r < CL; ++r) {
-                    const RegShared *o = cl.map_shared_rank(&sh, r);
-                    c[i] += o->cnt[lo + b];
-                    if (masses) m[i] += o->mass[lo + b];
-                }
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r)
+                    if (r < CL) {
+                        const RegShared *o = cl.map_shared_rank(&sh, r);
+                        c[i] += o->cnt[lo + b];
+                        if (masses) m[i] += o->mass[lo + b];
+                    }
             }
             csum += c[i];
             msum += m[i];
         }
-        // exclusive scan over the block
         uint32_t cs = csum;
         u64 ms = msum;
         for (int o = 1; o < 32; o <<= 1) {
@@ -446,7 +651,6 @@ __global__ void __launch_bounds__(kRegThreads) sample_kernel(SampleArgs a, int I
             if (r < rank) { cb += sh.x_cnt[r]; mb += sh.x_mass[r]; }
             total += sh.x_mass[r];
         }
-        if (all_mass) *all_mass = total;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i < per && tid * per + i < share && !reached(cb, mb, total) && reached(cb + c[i], mb + m[i], total)) {
@@ -456,6 +660,7 @@ __global__ void __launch_bounds__(kRegThreads) sample_kernel(SampleArgs a, int I
                     o->found_before = cb;
                     o->found_cnt = c[i];
                     o->found_mass = mb;
+                    o->goal = total;
                 }
             }
             cb += c[i];
@@ -469,237 +674,238 @@ __global__ void __launch_bounds__(kRegThreads) sample_kernel(SampleArgs a, int I
         __syncthreads();
     };
 
-    if ((by_k || by_p) && !isinf(wt.top)) {
-        // ---- candidates by distance from the top: 64 bins per unit of l / T
-        const float scale = fminf(64.f / t, 1e30f);
-        auto bin_of = [&](uint32_t ky) { return (int)fminf((wt.top - key_logit(ky)) * scale, (float)(kBins - 1)); };
-        clear_bins();
-        each([&](uint32_t ky, int) {
-            if (!ky) return;
-            const int b = bin_of(ky);
-            atomicAdd(&sh.cnt[b], 1u);
-            if (!by_k) atomicAdd(&sh.mass[b], wt.whole(wt.real(key_logit(ky))));
+    bool done_p = !by_p;
+    if (by_p && !by_k && top < INFINITY) {
+        // ---- top-p alone: masses by distance from the top
+        const float scale = fminf(128.f / t, 1e30f);
+        auto bin_of = [&](float f) { return f == top ? 0 : (int)fminf((top - f) * scale, (float)(kBins - 1)); };
+        for (int i = tid; i < 3 * kBins; i += kRegThreads) sh.part[0][i] = 0;
+        __syncthreads();
+        // a block's sum of 2^14 parts of 15 bits fits 32 bits.  The last bin
+        // (16 units and more below the top) may hold most of a row: summed in
+        // registers
+        u64 rest = 0;
+        each([&](float f, int) {
+            const int b = bin_of(f);
+            const u64 w = wt.whole(f);
+            if (b == kBins - 1) rest += w;
+            else if (w) {
+                atomicAdd(&sh.part[0][b], (uint32_t)w & 0x7fffu);
+                atomicAdd(&sh.part[1][b], (uint32_t)(w >> 15) & 0x3fffu);
+                atomicAdd(&sh.part[2][b], (uint32_t)(w >> 29));
+            }
         });
+        rest = reg_block_sum(rest, sh.tmp64);
+        if (tid < CL) cl.map_shared_rank(&sh, tid)->x_sum[rank] = rest;
+        cl.sync();
+        // every block sums a share of the bins, consecutive ones per thread
+        const int share = kBins / CL, per = max(share / kRegThreads, 1), lo = rank * share;
+        u64 m[4] = {0, 0, 0, 0}, msum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = tid * per + i;
+            if (i < per && b < share)
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r)
+                    if (r < CL) {
+                        const RegShared *o = cl.map_shared_rank(&sh, r);
+                        m[i] += (u64)o->part[0][lo + b] + ((u64)o->part[1][lo + b] << 15) +
+                                ((u64)o->part[2][lo + b] << 29);
+                    }
+            msum += m[i];
+        }
+        u64 block_mass;
+        u64 at = reg_block_scan(msum, sh.tmp64, block_mass);
+        if (tid < CL) cl.map_shared_rank(&sh, tid)->x_mass[rank] = block_mass;
+        if (tid == 0) sh.found_bin = 0xffffffffu;
+        cl.sync();
         u64 all = 0;
-        const bool found = find_bin(
-            [&](uint32_t c, u64 m, u64 total) {
-                return by_k ? c >= (uint32_t)k : c > 0 && (double)m >= (double)p * (double)total;
-            },
-            !by_k, 0, 0, &all);
-        const uint32_t n = sh.found_before + sh.found_cnt;
-        if (found && n <= kListMax && sh.found_bin < kBins - 1) {
-            // ---- gather them in block 0
-            RegShared *home = cl.map_shared_rank(&sh, 0);
-            const int edge = (int)sh.found_bin;
-            each([&](uint32_t ky, int i) {
-                if (!ky || bin_of(ky) > edge) return;
-                const uint32_t at = atomicAdd(&home->list_n, 1u);
-                home->list_key[at] = ky;
-                home->list_idx[at] = i;
+        for (int r = 0; r < CL; ++r) {
+            if (r < rank) at += sh.x_mass[r];
+            all += sh.x_mass[r] + sh.x_sum[r];
+        }
+        const double target = (double)p * (double)all;
+        auto reached = [&](u64 mass) { return mass > 0 && (double)mass >= target; };    // the top is in bin 0
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i < per && tid * per + i < share && !reached(at) && reached(at + m[i]))
+                for (int r = 0; r < CL; ++r) {
+                    RegShared *o = cl.map_shared_rank(&sh, r);
+                    o->found_bin = lo + tid * per + i;
+                    o->found_mass = at;
+                }
+            at += m[i];
+        }
+        cl.sync();
+        if (sh.found_bin != 0xffffffffu) {
+            const int bin = (int)sh.found_bin;
+            each([&](float f, int i) {
+                if (bin_of(f) == bin) gather(f, i);
             });
             cl.sync();
-            if (rank != 0) return;
-            if (tid < n) {
-                sh.list_w[tid] = wt.whole(wt.real(key_logit(sh.list_key[tid])));
-            }
-            __syncthreads();
-            // rank and mass before, pairwise: one candidate per thread
-            uint32_t place = 0;
-            u64 before = 0, w = 0;
-            uint32_t ky = 0;
-            int32_t idx = 0;
-            if (tid < n) {
-                ky = sh.list_key[tid];
-                idx = sh.list_idx[tid];
-                w = sh.list_w[tid];
-                for (uint32_t j = 0; j < n; ++j) {
-                    const uint32_t kj = sh.list_key[j];
-                    if (kj > ky || (kj == ky && sh.list_idx[j] < idx)) {
-                        ++place;
-                        before += sh.list_w[j];
+            if (rank == 0) {
+                const uint32_t n = sh.list_n;
+                float c = -INFINITY;
+                int l = -1;
+                if (n <= kListMax) {
+                    sort_descending(sh.list, sh.sorted, (int)n);
+                    const u64 id = tid < n ? sh.sorted[tid] : 0;
+                    u64 total;
+                    const u64 before = reg_block_scan(tid < n ? wt.whole(logit_of(id)) : 0, sh.tmp64, total);
+                    const bool keep = tid < n && ((tid == 0 && bin == 0) || (double)(sh.found_mass + before) < target);
+                    // the kept ones come first: the last of them is the cut
+                    const uint32_t kept = reg_block_sum(keep ? 1u : 0u, sh.tmp32);
+                    if (keep && tid == kept - 1) {
+                        sh.cut = logit_of(id);
+                        sh.last = (int)~(uint32_t)id;
                     }
+                    __syncthreads();
+                    c = sh.cut;
+                    l = sh.last;
+                    __syncthreads();
                 }
-            }
-            bool keep = tid < n && (!by_k || place < (uint32_t)k);
-            if (by_p) {
-                const u64 total = by_k ? reg_block_sum(keep ? w : 0ull, sh.tmp64) : all;
-                keep = keep && (place == 0 || (double)before < (double)p * (double)total);
-            }
-            keep = keep && (wt.min_w == 0.0 || wt.real(key_logit(ky)) >= wt.min_w);
-            if (!keep) w = 0;
-            if (tid < n) sh.list_keep[tid] = w;
-            const u64 total = reg_block_sum(w, sh.tmp64);     // synchronises
-            const float u = a.uniform[row];
-            const u64 goal = min((u64)((double)(u > 0.f ? fminf(u, 1.f) : 0.f) * (double)total), total - 1);
-            if (w > 0) {
-                u64 run = 0;
-                for (uint32_t j = 0; j < n; ++j)
-                    if (sh.list_idx[j] < idx) run += sh.list_keep[j];
-                if (run <= goal && goal < run + w) a.token[row] = idx;
-            }
-            return;
-        }
-        // ---- the exact cuts, by count and by mass
-        for (int stage = 0; stage < 2; ++stage) {
-            const bool by_mass = stage == 1;
-            if (by_mass ? !by_p : !by_k) continue;
-            double target = 0.0;
-            if (by_mass) {
-                u64 m = 0;
-                uint32_t eq = 0;
-                each([&](uint32_t ky, int) {
-                    if (ky > cut) m += wt.whole(wt.real(key_logit(ky)));
-                    eq += ky == cut;
-                });
-                const u64 bm = reg_block_sum(m, sh.tmp64);
-                const uint32_t be = reg_block_sum(eq, sh.tmp32);
-                cl.sync();
                 if (tid < CL) {
                     RegShared *o = cl.map_shared_rank(&sh, tid);
-                    o->x_sum[rank] = bm;
-                    o->x_cnt[rank] = be;
-                }
-                cl.sync();
-                u64 total = 0;
-                uint32_t n_eq = 0;
-                for (int r = 0; r < CL; ++r) { total += sh.x_sum[r]; n_eq += sh.x_cnt[r]; }
-                total += cut > 1u ? (u64)min(n_eq, ties) * wt.whole(wt.real(key_logit(cut))) : 0;
-                target = (double)p * (double)total;
-                cl.sync();
-            }
-            uint32_t lo = cut, hi = top_key, cnt_above = 0;
-            u64 mass_above = 0;
-            while (true) {
-                int bits = 0;
-                while ((hi - lo) >> bits >= kBins) ++bits;
-                clear_bins();
-                each([&](uint32_t ky, int) {
-                    if (ky < lo || ky > hi) return;
-                    const uint32_t b = (hi - ky) >> bits;
-                    atomicAdd(&sh.cnt[b], 1u);
-                    if (by_mass) atomicAdd(&sh.mass[b], wt.whole(wt.real(key_logit(ky))));
-                });
-                if (!find_bin([&](uint32_t c, u64 m, u64) { return by_mass ? c > 0 && (double)m >= target : c >= (uint32_t)k; },
-                              by_mass, cnt_above, mass_above, nullptr))
-                    break;      // fewer than k, or ties cut short the mass: all stay
-                cnt_above = sh.found_before;
-                mass_above = sh.found_mass;
-                hi -= sh.found_bin << bits;
-                const u64 span = ((u64)1 << bits) - 1;
-                if ((u64)(hi - lo) > span) lo = hi - (uint32_t)span;
-                if (lo == hi) {
-                    uint32_t need = (uint32_t)k - cnt_above;
-                    if (by_mass) {
-                        const double w = (double)wt.whole(wt.real(key_logit(lo)));
-                        const double n = w > 0 ? ceil((target - (double)mass_above) / w) : 1.0;
-                        need = n < 1.0 ? 1u : n > 4e9 ? 0xffffffffu : (uint32_t)n;
-                    }
-                    ties = lo == cut ? min(ties, need) : need;
-                    cut = lo;
-                    break;
+                    o->cut = c;
+                    o->last = l;
                 }
             }
+            cl.sync();
+            if (sh.last >= 0) {
+                cut = sh.cut;
+                last = sh.last;
+                done_p = true;
+            }
+            cl.sync();
         }
     }
 
-    // The index at which the running sum of weight(e, index), in index order,
-    // first exceeds the goal; goal_of(total) gives it.  One thread of the
-    // cluster calls done(index).
-    auto pick = [&](auto weight, auto goal_of, auto done) {
-        __syncthreads();
-#pragma unroll 1
+    // The index at which the running sum of weight(logit, index), in index
+    // order, first exceeds goal(total).  One thread of the cluster calls
+    // done(index).  Logits below `least` weigh nothing.
+    auto pick = [&](float least, auto weight, auto goal, auto done) {
+        u64 s = 0;
+#pragma unroll 2
         for (int it = 0; it < IT; ++it) {
-            const uint4 q = keys[it * kRegThreads + tid];
-            const int i = base + it * kVecStep + 4 * tid;
-            u64 s = weight(q.x, i) + weight(q.y, i + 1) + weight(q.z, i + 2) + weight(q.w, i + 3);
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane == 0) sh.sub[it * kRegWarps + warp] = s;
+            const float4 q = xs[it * kRegThreads + tid];
+            const int i = base + it * 128;
+            if (fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)) >= least)
+                s += weight(q.x, i) + weight(q.y, i + 1) + weight(q.z, i + 2) + weight(q.w, i + 3);
         }
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         __syncthreads();
-        // warp 0: sums over (it, warp), N consecutive ones a lane
-        const int N = (IT * kRegWarps + 31) / 32;
-        if (warp == 0) {
-            u64 s = 0;
-            for (int i = 0; i < N; ++i) s += lane * N + i < IT * kRegWarps ? sh.sub[lane * N + i] : 0;
-            u64 run = s;
-            for (int o = 1; o < 32; o <<= 1) {
-                const u64 y = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += y;
-            }
-            const u64 mine = __shfl_sync(0xffffffffu, run, 31);
-            if (lane < CL) cl.map_shared_rank(&sh, lane)->x_sum[rank] = mine;
-            sh.tmp64[0] = mine;
+        if (lane == 0) sh.sub[warp] = s;
+        __syncthreads();
+        u64 mine = 0, warp_before = 0;
+#pragma unroll
+        for (int w = 0; w < kRegWarps; ++w) {
+            if (w == warp) warp_before = mine;
+            mine += sh.sub[w];
         }
+        if (tid < CL) cl.map_shared_rank(&sh, tid)->x_sum[rank] = mine;
         cl.sync();
         u64 total = 0, before = 0;
         for (int r = 0; r < CL; ++r) {
             if (r == rank) before = total;
             total += sh.x_sum[r];
         }
-        const u64 goal = goal_of(total);
-        const bool here = goal >= before && goal < before + sh.x_sum[rank];
-        if (here) {       // the same answer for the whole block
-            if (warp == 0) {
-                u64 s = 0;
-                for (int i = 0; i < N; ++i) s += lane * N + i < IT * kRegWarps ? sh.sub[lane * N + i] : 0;
-                u64 run = s;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const u64 y = __shfl_up_sync(0xffffffffu, run, o);
-                    if (lane >= o) run += y;
-                }
-                run += before - s;
-                for (int i = 0; i < N; ++i) {
-                    const u64 w = lane * N + i < IT * kRegWarps ? sh.sub[lane * N + i] : 0;
-                    if (goal >= run && goal < run + w) {
-                        sh.hit = lane * N + i;
-                        sh.goal = goal - run;
-                    }
-                    run += w;
-                }
+        const u64 g = goal(total);
+        u64 run = before + warp_before;
+        if (g < run || g >= run + s) return;       // the same answer for the whole warp
+        for (int it = 0; it < IT; ++it) {
+            const float4 q = xs[it * kRegThreads + tid];
+            const int i = base + it * 128;
+            const u64 w[4] = {weight(q.x, i), weight(q.y, i + 1), weight(q.z, i + 2), weight(q.w, i + 3)};
+            const u64 own = w[0] + w[1] + w[2] + w[3];
+            u64 at = own;
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 y = __shfl_up_sync(0xffffffffu, at, o);
+                if (lane >= o) at += y;
             }
-            __syncthreads();
-            if (sh.hit % kRegWarps == warp) {
-                const int it = sh.hit / kRegWarps, i = base + it * kVecStep + 4 * tid;
-                const uint4 q = keys[it * kRegThreads + tid];
-                const u64 w[4] = {weight(q.x, i), weight(q.y, i + 1), weight(q.z, i + 2), weight(q.w, i + 3)};
-                u64 run = w[0] + w[1] + w[2] + w[3];
-                const u64 mine = run;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const u64 y = __shfl_up_sync(0xffffffffu, run, o);
-                    if (lane >= o) run += y;
-                }
-                run -= mine;
+            const u64 all = __shfl_sync(0xffffffffu, at, 31);
+            if (g >= run + all) {
+                run += all;
+                continue;
+            }
+            at += run - own;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (sh.goal >= run && sh.goal < run + w[c]) done(i + c);
-                    run += w[c];
-                }
+            for (int c = 0; c < 4; ++c) {
+                if (g >= at && g < at + w[c]) done(i + c);
+                at += w[c];
             }
+            return;
         }
     };
 
-    int32_t last = 0x7fffffff;    // ties up to this index stay
-    if (ties != 0xffffffffu) {
-        if (tid == 0) sh.tie_last = 0x7fffffff;
-        cl.sync();
-        pick([&](uint32_t ky, int) { return ky == cut ? 1ull : 0ull; }, [&](u64) { return (u64)ties - 1; },
-             [&](int i) {
-                 for (int r = 0; r < CL; ++r) cl.map_shared_rank(&sh, r)->tie_last = i;
-             });
-        cl.sync();
-        last = sh.tie_last;
+    // ---- the exact cuts, by count and by mass, where nothing above found them
+    for (int stage = 0; stage < 2; ++stage) {
+        const bool by_mass = stage == 1;
+        if (by_mass ? done_p : !by_k) continue;
+        double target = 0.0;
+        if (by_mass) {
+            u64 m = 0;
+            each([&](float f, int i) {
+                if (f > cut || (f == cut && i <= last)) m += wt.whole(f);
+            });
+            m = reg_block_sum(m, sh.tmp64);
+            cl.sync();
+            if (tid < CL) cl.map_shared_rank(&sh, tid)->x_sum[rank] = m;
+            cl.sync();
+            u64 total = 0;
+            for (int r = 0; r < CL; ++r) total += sh.x_sum[r];
+            target = (double)p * (double)total;
+            cl.sync();
+        }
+        uint32_t lo = max(logit_key(cut), 1u), hi = logit_key(top), cnt_above = 0;
+        u64 mass_above = 0;
+        while (true) {
+            int bits = 0;
+            while ((hi - lo) >> bits >= kBins) ++bits;
+            clear_bins();
+            each([&](float f, int i) {
+                const uint32_t ky = logit_key(f);
+                if (ky < lo || ky > hi || (f == cut && i > last)) return;
+                const uint32_t b = (hi - ky) >> bits;
+                atomicAdd(&sh.cnt[b], 1u);
+                if (by_mass) atomicAdd(&sh.mass[b], wt.whole(f));
+            });
+            if (!find_bin(
+                    [&](uint32_t c, u64 m, u64) { return by_mass ? c > 0 && (double)m >= target : c >= (uint32_t)k; },
+                    by_mass, cnt_above, mass_above))
+                break;      // fewer than k: all stay
+            cnt_above = sh.found_before;
+            mass_above = sh.found_mass;
+            hi -= sh.found_bin << bits;
+            const u64 span = ((u64)1 << bits) - 1;
+            if ((u64)(hi - lo) > span) lo = hi - (uint32_t)span;
+            if (lo != hi) continue;
+            uint32_t need = (uint32_t)k - cnt_above;      // of the equal ones
+            if (by_mass) {
+                const double w = (double)wt.whole(key_logit(lo));
+                const double n = w > 0 ? ceil((target - (double)mass_above) / w) : 1.0;
+                need = n < 1.0 ? 1u : n > 4e9 ? 0xffffffffu : (uint32_t)n;
+            }
+            const int32_t old = key_logit(lo) == cut ? last : 0x7fffffff;
+            cut = key_logit(lo);
+            last = old;
+            if (need < sh.found_cnt) {     // up to the need-th in index order
+                cl.sync();
+                pick(cut, [&](float f, int i) { return f == cut && i <= old ? 1ull : 0ull; },
+                     [&](u64) { return (u64)need - 1; },
+                     [&](int i) {
+                         for (int r = 0; r < CL; ++r) cl.map_shared_rank(&sh, r)->last = i;
+                     });
+                cl.sync();
+                last = sh.last;
+            }
+            break;
+        }
     }
+
     const float u = a.uniform[row];
-    pick(
-        [&](uint32_t ky, int i) {
-            if (ky < cut || ky == 0 || (ky == cut && i > last)) return 0ull;
-            const double w = wt.real(key_logit(ky));
-            return w >= wt.min_w ? wt.whole(w) : 0ull;
-        },
-        [&](u64 total) {
-            return min((u64)((double)(u > 0.f ? fminf(u, 1.f) : 0.f) * (double)total), total - 1);
-        },
-        [&](int i) { a.token[row] = i; });
+    const float least = fmaxf(cut, wt.floor);
+    pick(least, [&](float f, int i) { return f < least || (f == cut && i > last) ? 0ull : wt.final_whole(f); },
+         [&](u64 total) { return goal_of(u, total); }, [&](int i) { a.token[row] = i; });
     cl.sync();    // nobody leaves while its memory may still be written
 }
 
