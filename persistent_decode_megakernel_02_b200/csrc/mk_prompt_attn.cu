@@ -28,6 +28,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "mk_tc.cuh"
 
@@ -36,7 +37,50 @@ namespace {
 
 constexpr int kTile = 128;                 // query rows of a unit, keys of a tile
 constexpr int kPromptThreads = 384;
+// Registers: launched at 168 a thread (65536 / 384, rounded down to 8), moved
+// from the control warpgroup to the softmax ones, whose row of S stays in
+// registers.  The shares must add up to the launch's, or the wait for more
+// registers would not end: prompt_launch refuses any other launch count.
+constexpr int kLaunchRegsPrompt = 168, kSoftmaxRegs = 208, kControlRegsPrompt = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kControlRegsPrompt == kPromptThreads * kLaunchRegsPrompt, "register split");
+// One quarter of the pairs' first halves go to ex2_fma (of the exponentials:
+// one eighth); 0, 1/4, 1/2, 3/4 of them: 489, 479, 480, 485 us at 8192 tokens.
+constexpr int kPolyNum = 1, kPolyOf = 4;
 constexpr float kRescale = 8.f;            // exponent headroom before O is rescaled
+
+// The larger of three, NaN if one is NaN.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// 2^x of a pair by multiplications and additions, for x <= 127 (results below
+// 2^-126 are given as 2^-126; not for NaN): the nearest integer by adding
+// 1.5 * 2^23, and a polynomial for the rest in [-1/2, 1/2] whose relative
+// error is least at its degree (3: 7.5e-5, for weights rounded to bf16; 4:
+// 2.6e-6, for fp16).
+template <int DEG>
+__device__ __forceinline__ float2 ex2_fma(float2 x) {
+    x.x = fmaxf(x.x, -126.f);
+    x.y = fmaxf(x.y, -126.f);
+    auto two = [](float v) { return make_float2(v, v); };
+    const float2 n = fadd2(x, two(12582912.f));
+    const float2 f = fadd2(n, two(-12582912.f));
+    const float2 r = ffma2(f, two(-1.f), x);
+    float2 p;
+    if constexpr (DEG == 3) {
+        p = ffma2(r, two(0.0551716685295105f), two(0.2426111251115799f));
+        p = ffma2(r, p, two(0.6932609677314758f));
+        p = ffma2(r, p, two(0.9999280571937561f));
+    } else {
+        p = ffma2(r, two(0.009570102207362652f), two(0.05591785907745361f));
+        p = ffma2(r, p, two(0.240247443318367f));
+        p = ffma2(r, p, two(0.6931217908859253f));
+        p = ffma2(r, p, two(0.9999992847442627f));
+    }
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(n.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(n.y) << 23)));
+}
 
 template <int D>
 struct PromptSmem {
@@ -143,6 +187,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
     tc_fence_after();
     const uint32_t tmem = t.tmem;
 
+    if (warp >= 8) set_regs_down<kControlRegsPrompt>();
     if (warp == 8) {
         if (lane == 0) {
             // ---- loader: Q, then K0 V0 K1 V1 ...
@@ -170,55 +215,65 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
             }
         }
     } else if (warp == 9) {
-        if (lane == 0) {
-            // ---- MMA issuer
-            const uint32_t ring = smem_addr(smem + L::kRing), qs = smem_addr(smem + L::kQ);
-            constexpr uint32_t kIdS = f16_idesc(kBf16, false, kTile, kTile);
-            constexpr uint32_t kIdO = f16_idesc(kBf16, true, kTile, D);
-            auto qk = [&](int u, int f) {
-                const uint32_t kb = ring + f % L::kStages * L::kTileBytes, qb = qs + u * L::kTileBytes;
-                #pragma unroll
+        // ---- MMA issuer: the whole warp walks the loop (addresses stay
+        // uniform), one elected thread issues.  With a single thread walking
+        // it, every operand went through a vector register first: 78 cycles
+        // an instruction instead of the 64 it computes.
+        const bool leader = elect_one();
+        const uint32_t ring = (smem_addr(smem + L::kRing) & 0x3FFFFu) >> 4, qs = (smem_addr(smem + L::kQ) & 0x3FFFFu) >> 4;
+        constexpr uint32_t kIdS = f16_idesc(kBf16, false, kTile, kTile);
+        constexpr uint32_t kIdO = f16_idesc(kBf16, true, kTile, D);
+        auto qk = [&](int u, int f) {
+            const uint32_t kb = ring + (f % L::kStages) * (L::kTileBytes >> 4), qb = qs + u * (L::kTileBytes >> 4);
+            if (leader) {
+#pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t off = (s >> 2) * kTile * 128 + (s & 3) * 32;
-                    mma_ss(tmem + u * kTile, desc_sw128(qb + off, 16, 1024), desc_sw128(kb + off, 16, 1024), kIdS,
+                    const uint32_t off = ((s >> 2) * kTile * 128 + (s & 3) * 32) >> 4;
+                    mma_ss(tmem + u * kTile, desc_sw128_at(qb + off, 16, 1024), desc_sw128_at(kb + off, 16, 1024), kIdS,
                            s > 0);
                 }
                 tc_commit(&t.s_full[u]);
-            };
-            auto pv = [&](int u, int f, bool first) {
-                const uint32_t vb = ring + f % L::kStages * L::kTileBytes;
+            }
+        };
+        auto pv = [&](int u, int f, bool first, bool last) {
+            const uint32_t vb = ring + (f % L::kStages) * (L::kTileBytes >> 4);
+            if (leader) {
+#pragma unroll
                 for (int s = 0; s < kTile / 16; ++s)
                     mma_ts(tmem + 2 * kTile + u * D, tmem + u * kTile + s * 8,
-                           desc_sw128(vb + s * 16 * 128, kTile * 128, 1024), kIdO, !first || s > 0);
-            };
-            auto full = [&](int f) { return mbar_wait(&t.full[f % L::kStages], (f / L::kStages) & 1, &t.abort); };
-            bool ok = mbar_wait(&t.q_full, 0, &t.abort) && full(0);
-            if (ok) {
-                qk(0, 0);
-                if (two) qk(1, 0);
-                tc_commit(&t.empty[0]);
+                           desc_sw128_at(vb + (s * 16 * 128 >> 4), kTile * 128, 1024), kIdO, s > 0 || !first);
+                if (last) tc_commit(&t.o_full[u]);
             }
-            for (int j = 0; j < J && ok; ++j) {
-                const int fv = 2 * j + 1, fk = 2 * j + 2;
-                ok = full(fv);
-                if (!ok) break;
-                if (j >= blk0) mbar_arrive(&t.guard_go[j - blk0]);   // a masked tile (the last, or last two)
-                for (int u = 0; u < 2 && ok; ++u) {
-                    const int n = u ? n1 : n0;
-                    if (j >= n) continue;
-                    ok = mbar_wait(&t.p_ready[u], j & 1, &t.abort);
-                    if (!ok) break;
-                    if (j >= blk0) ok = mbar_wait(&t.guard_done[j - blk0], 0, &t.abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    pv(u, fv, j == 0);
-                    if (j + 1 < n) {
-                        ok = full(fk);
-                        if (ok) qk(u, fk);
-                    } else
-                        tc_commit(&t.o_full[u]);
+        };
+        auto full = [&](int f) {
+            return mbar_wait_warp(&t.full[f % L::kStages], (f / L::kStages) & 1, &t.abort);
+        };
+        bool ok = mbar_wait_warp(&t.q_full, 0, &t.abort) && full(0);
+        if (ok) {
+            qk(0, 0);
+            if (two) qk(1, 0);
+            if (leader) tc_commit(&t.empty[0]);
+        }
+        for (int j = 0; j < J && ok; ++j) {
+            const int fv = 2 * j + 1, fk = 2 * j + 2;
+            ok = full(fv);
+            if (!ok) break;
+            if (j >= blk0 && leader) mbar_arrive(&t.guard_go[j - blk0]);   // a masked tile (the last, or last two)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int n = u ? n1 : n0;
+                if (j >= n || !ok) continue;
+                ok = mbar_wait_warp(&t.p_ready[u], j & 1, &t.abort);
+                if (ok && j >= blk0) ok = mbar_wait_warp(&t.guard_done[j - blk0], 0, &t.abort);
+                if (!ok) continue;
+                tc_fence_after();
+                pv(u, fv, j == 0, j + 1 == n);
+                if (j + 1 < n) {
+                    ok = full(fk);
+                    if (ok) qk(u, fk);
                 }
-                if (!ok) break;
+            }
+            if (ok && leader) {
                 tc_commit(&t.empty[fv % L::kStages]);
                 if (j + 1 < J) tc_commit(&t.empty[fk % L::kStages]);
             }
@@ -264,6 +319,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
         }
     } else {
         // ---- softmax: one row per thread
+        set_regs_up<kSoftmaxRegs>();
         const int u = warp >> 2, r = tid & 127;
         const int n = u ? n1 : n0, blk = u ? blk1 : blk0, head = u ? head1 : head0;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // lane 32 (w % 4) in bits 16..
@@ -277,55 +333,78 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
             ok = mbar_wait_warp(&t.s_full[u], j & 1, &t.abort);
             if (!ok) break;
             tc_fence_after();
-            const int limit = j == blk ? r : kTile;   // keys beyond it are not seen
-            float top = -INFINITY;
-            uint32_t x[32];
-            for (int q = 0; q < 4; ++q) {
-                tmem_ld32(ts + q * 32, x);
-                tmem_ld_wait();
+            uint32_t x[4][32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (q * 32 + i <= limit) top = fmaxf(top, __uint_as_float(x[i]));
-            }
+            for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, x[q]);
+            tmem_ld_wait();
+            if (j == blk)      // the diagonal: keys beyond the row's own are not seen
+#pragma unroll
+                for (int i = 0; i < kTile; ++i)
+                    if (i > r) x[i / 32][i % 32] = 0xff800000u;
+            auto at = [&](int i) { return __uint_as_float(x[i / 32][i % 32]); };
+            float top4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top4[i] = max3_nan(at(i), at(i + 4), at(i + 8));
+#pragma unroll
+            for (int i = 12; i < kTile - 4; i += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top4[k] = max3_nan(top4[k], at(i + k), at(i + k + 4));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top4[k] = max3_nan(top4[k], at(kTile - 4 + k), top4[k]);
+            const float top = max3_nan(max3_nan(top4[0], top4[1], top4[2]), top4[3], top4[3]);
             const float old = m;
             if (!((top - m) * c <= kRescale)) m = fmaxf(m, top);
             const bool raise = m != old;
             if (__any_sync(0xffffffffu, raise)) {
-                const float f = raise ? exp2f((old - m) * c) : 1.f;
+                const float f = raise ? ex2((old - m) * c) : 1.f;
                 l *= f;
-                if (j > 0) {
-                    for (int q = 0; q < D / 32; ++q) {
-                        tmem_ld32(to + q * 32, x);
+                if (j > 0)
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t o[16];
+                        tmem_ld16(to + q * 16, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                        tmem_st32(to + q * 32, x);
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st16(to + q * 16, o);
                     }
-                }
             }
             const float mc = m == -INFINITY ? 0.f : m * c;
-            float sum = 0.f;
-            for (int q = 0; q < 4; ++q) {
-                tmem_ld32(ts + q * 32, x);
-                tmem_ld_wait();
-                uint32_t w[16];
+            const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+            auto weights = [&](auto mixed) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    float e0 = exp2f(fmaf(__uint_as_float(x[i]), c, -mc));
-                    float e1 = exp2f(fmaf(__uint_as_float(x[i + 1]), c, -mc));
-                    if (q * 32 + i > limit) e0 = 0.f;
-                    if (q * 32 + i + 1 > limit) e1 = 0.f;
-                    sum += e0 + e1;
-                    w[i / 2] = T::pack(e0, e1);
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        float2 e0 = ffma2(make_float2(at(q * 32 + i), at(q * 32 + i + 1)), c2, mc2);
+                        float2 e1 = ffma2(make_float2(at(q * 32 + i + 2), at(q * 32 + i + 3)), c2, mc2);
+                        if (mixed.value && (i / 4) % kPolyOf < kPolyNum) {
+                            e0 = ex2_fma<kBf16 ? 3 : 4>(e0);
+                        } else {
+                            e0.x = ex2(e0.x);
+                            e0.y = ex2(e0.y);
+                        }
+                        e1.x = ex2(e1.x);
+                        e1.y = ex2(e1.y);
+                        sum0 = fadd2(sum0, e0);
+                        sum1 = fadd2(sum1, e1);
+                        w[i / 2] = T::pack(e0.x, e0.y);
+                        w[i / 2 + 1] = T::pack(e1.x, e1.y);
+                    }
+                    tmem_st16(ts + q * 16, w);      // P, over what this row has read of S
                 }
-                // columns 16 q.. of P: behind what this row has read of S
-                tmem_st16(ts + q * 16, w);
-            }
-            l += sum;
+            };
+            // masked scores have to give exactly zero: the function unit alone
+            if (j == blk) weights(std::false_type());
+            else weights(std::true_type());
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&t.p_ready[u]);
+            l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+            if (top != top) l = NAN;      // a score that is not a number
         }
         if (ok && n > 0) ok = mbar_wait_warp(&t.o_full[u], 0, &t.abort);
         if (ok && n > 0) {
@@ -415,6 +494,10 @@ cudaError_t launch(const PromptParams &p, int device, int grid, cudaStream_t str
         const cudaError_t e = cudaFuncSetAttribute(prompt_attn_kernel<T, D>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem<D>::kBytes);
         if (e != cudaSuccess) return e;
+        cudaFuncAttributes at;
+        const cudaError_t f = cudaFuncGetAttributes(&at, prompt_attn_kernel<T, D>);
+        if (f != cudaSuccess) return f;
+        if (at.numRegs != kLaunchRegsPrompt) return cudaErrorInvalidDeviceFunction;
         ready[device].store(true, std::memory_order_relaxed);
     }
     prompt_attn_kernel<T, D><<<grid, kPromptThreads, PromptSmem<D>::kBytes, stream>>>(p);

@@ -25,9 +25,15 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
 // stride offset is that of the 8-row groups; for an MN-major one (rows run
 // along K) it is that of 8 K-rows, and the leading offset separates blocks of
 // 64 elements along MN.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// `at` is the shared-memory address / 16; the high word is a constant.
+__device__ __forceinline__ uint64_t desc_sw128_at(uint32_t at, uint32_t lbo, uint32_t sbo) {
+    return ((uint64_t)((sbo >> 4) | 1u << 14 | 2u << 29) << 32) | (at | (lbo >> 4) << 16);
+}
+// One thread of the warp (all 32 lanes call it).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
 }
 // Instruction descriptor of kind::f16: fp32 accumulator, both operands bf16
 // (or both fp16), A K-major, B K-major or MN-major.
@@ -79,7 +85,7 @@ __device__ __forceinline__ void fence_mbar_init() {
 // Wait for a barrier's phase, bounded: after `kWaitNs` (or once another role
 // of the block has given up) it returns false with *abort set.
 constexpr unsigned long long kWaitNs = 2000000000ull;
-static __device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort) {
     const unsigned long long t0 = globaltimer();
     while (true) {
         for (int i = 0; i < 64; ++i)
