@@ -1,11 +1,16 @@
 // mk_prompt_attn.cu -- causal attention over packed prompts with grouped
 // heads, on the tcgen05 tensor cores.
 //
-// Work is cut into units of (128 query rows of a sequence, query head); a
-// block takes two units of one KV head, in the order (row block, head of the
-// group), so that both share the K and V tiles they stream (128 keys each).
-// A unit at row block b needs key tiles 0..b, the last one masked along its
-// diagonal (row blocks and key tiles both start at the sequence's start).
+// Work is cut into units of (128 query rows of a sequence, query head); an
+// item is two units of one KV head that share the K and V tiles they stream
+// (128 keys each): two heads of a row block, or, where the group is odd,
+// neighbours in the order (row block, head) of two row blocks.  A unit at row
+// block b needs key tiles 0..b, the last one masked along its diagonal (row
+// blocks and key tiles both start at the sequence's start).  One block per SM
+// walks the items, longest first over all sequences, in a there-and-back
+// order (block c takes c, 2P - 1 - c, 2P + c, ...), which needs no counter and
+// leaves the blocks' sums close; the next item's loads and first products
+// start while the last one's outputs are written.
 //
 // Per unit and key tile j:
 //   S = Q K_j^T          (tcgen05, fp32 in tensor memory, M = N = 128)
@@ -89,17 +94,30 @@ struct PromptSmem {
     static constexpr int kQ = 0;
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kTail = kRing + kStages * kTileBytes;
-    static constexpr int kBytes = kTail + 2560 + 1024;   // barriers, poison; slack to align the base
+    static constexpr int kBytes = kTail + 4096 + 1024;   // barriers, items; slack to align the base
 };
 
+struct PromptItem {
+    int row0, len;                 // the sequence's first row and length; len 0: no more items
+    int kvh, tiles;                // key tiles of the longer unit
+    int blk[2], head[2], n[2];     // per unit: row block, query head, key tiles (0: no such unit)
+};
+
+// Every barrier's phases run on from item to item.
 struct PromptTail {
-    uint64_t q_full, full[8], empty[8], s_full[2], p_ready[2], o_full[2], guard_go[2], guard_done[2];
+    uint64_t full[8], empty[8];               // the ring of K and V tiles
+    uint64_t q_full, q_empty;                 // both units' queries
+    uint64_t s_full[2], p_ready[2];           // per tile
+    uint64_t o_full[2], o_empty[2];           // per item
+    uint64_t guard_go[2], guard_done[2];      // the first and second masked tile of an item
+    uint64_t item_full[2], item_empty[2];
+    PromptItem item[2];
     uint32_t tmem;
     int abort;
-    int any;             // a value was taken out
-    int first[3][128];   // per column: first key (of the sequence) with NaN, +inf, -inf
+    int any[2];             // a value was taken out
+    int first[2][3][128];   // per column: first key (of the sequence) with NaN, +inf, -inf
 };
-static_assert(sizeof(PromptTail) <= 2560, "tail of the shared memory");
+static_assert(sizeof(PromptTail) <= 4096, "tail of the shared memory");
 
 struct PromptParams {
     CUtensorMap q, k, v;
@@ -115,104 +133,146 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
     PromptTail &t = *reinterpret_cast<PromptTail *>(smem + L::kTail);
     const PromptArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = a.nq / a.nkv;
 
-    // ---- the block's work: item `it` of a sequence, for KV head kvh
     if (blockIdx.x == 0)
         for (int i = tid; i < a.n_seqs; i += kPromptThreads) {
             const int b = a.cu[i], e = a.cu[i + 1];
             if (b < 0 || e < b || e > a.n_tokens || e - b > a.max_len) bad_value(a.status);
         }
-    const int kvh = blockIdx.x % a.nkv;
-    int it = blockIdx.x / a.nkv;
-    int row0 = 0, len = 0, items = 0;
-    for (int s0 = 0; s0 < a.n_seqs && items == 0; s0 += 32) {
-        int b = 0, n = 0;
-        if (s0 + lane < a.n_seqs) {
-            b = a.cu[s0 + lane];
-            const int e = a.cu[s0 + lane + 1];
-            if (b >= 0 && e >= b && e <= a.n_tokens && e - b <= a.max_len) n = e - b;
-        }
-        const int mine = ((n + kTile - 1) / kTile * G + 1) / 2;
-        int sum = mine;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, sum > it);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            row0 = __shfl_sync(0xffffffffu, b, src);
-            len = __shfl_sync(0xffffffffu, n, src);
-            items = __shfl_sync(0xffffffffu, mine, src);
-            it -= __shfl_sync(0xffffffffu, sum - mine, src);
-        } else
-            it -= __shfl_sync(0xffffffffu, sum, 31);
-    }
-    if (items == 0) return;
-    it = items - 1 - it;   // the longest first
-    const int units = (len + kTile - 1) / kTile * G;
-    const int u0 = 2 * it;
-    const bool two = u0 + 1 < units;
-    const int blk0 = u0 / G, blk1 = two ? (u0 + 1) / G : blk0;
-    const int head0 = kvh * G + u0 % G, head1 = two ? kvh * G + (u0 + 1) % G : head0;
-    const int n0 = blk0 + 1, n1 = two ? blk1 + 1 : 0, J = two ? blk1 + 1 : n0;
 
     // ---- setup
     if (warp == 9) {
         if (lane == 0) {
-            mbar_init(&t.q_full, 1);
             for (int i = 0; i < L::kStages; ++i) {
                 mbar_init(&t.full[i], 1);
                 mbar_init(&t.empty[i], 1);
             }
+            mbar_init(&t.q_full, 1);
+            mbar_init(&t.q_empty, 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&t.s_full[i], 1);
                 mbar_init(&t.p_ready[i], 4);
                 mbar_init(&t.o_full[i], 1);
+                mbar_init(&t.o_empty[i], 4);
                 mbar_init(&t.guard_go[i], 1);
                 mbar_init(&t.guard_done[i], 2);
+                mbar_init(&t.item_full[i], 1);
+                mbar_init(&t.item_empty[i], 11);   // issuer, 2 guard and 8 softmax warps
+                t.any[i] = 0;
             }
             t.abort = 0;
-            t.any = 0;
             fence_mbar_init();
         }
         __syncwarp();
         tmem_alloc(&t.tmem, 512);
     }
     if (warp < 8)
-        for (int i = tid; i < 3 * 128; i += 256) t.first[i / 128][i % 128] = 0x7fffffff;
+        for (int i = tid; i < 2 * 3 * 128; i += 256) (&t.first[0][0][0])[i] = 0x7fffffff;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = t.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, t.tmem, 0);
 
     if (warp >= 8) set_regs_down<kControlRegsPrompt>();
     if (warp == 8) {
-        if (lane == 0) {
-            // ---- loader: Q, then K0 V0 K1 V1 ...
-            mbar_arrive_expect_tx(&t.q_full, (two ? 2 : 1) * L::kTileBytes);
-            for (int h = 0; h < D / 64; ++h) {
-                tma_load_3d(smem + L::kQ + h * kTile * 128, &p.q, h * 64, head0, row0 + blk0 * kTile, &t.q_full);
-                if (two)
-                    tma_load_3d(smem + L::kQ + L::kTileBytes + h * kTile * 128, &p.q, h * 64, head1,
-                                row0 + blk1 * kTile, &t.q_full);
+        // ---- scheduler and loader
+        const int G = a.nq / a.nkv, R = G & 1 ? 2 : 1;    // row blocks of a level
+        const int per_seq = G * R / 2 * a.nkv;            // items of a sequence at a level
+        int row0 = 0, len = 0;      // of sequence s0 + lane
+        auto levels_of = [&](int s) {
+            row0 = len = 0;
+            if (s < a.n_seqs) {
+                const int b = a.cu[s], e = a.cu[s + 1];
+                if (b >= 0 && e >= b && e <= a.n_tokens && e - b <= a.max_len) {
+                    row0 = b;
+                    len = e - b;
+                }
             }
-            bool ok = true;
-            for (int f = 0; f < 2 * J && ok; ++f) {
-                const int st = f % L::kStages, use = f / L::kStages;
-                if (use > 0) ok = mbar_wait(&t.empty[st], (use - 1) & 1, &t.abort);
-                if (!ok) break;
-                mbar_arrive_expect_tx(&t.full[st], L::kTileBytes);
+            return (len + kTile * R - 1) / (kTile * R);
+        };
+        auto count = [&](int level) {
+            int c = 0;
+            for (int s0 = 0; s0 < a.n_seqs; s0 += 32)
+                c += __popc(__ballot_sync(0xffffffffu, levels_of(s0 + lane) > level));
+            return c;
+        };
+        int level = 0;
+        for (int s0 = 0; s0 < a.n_seqs; s0 += 32) level = max(level, levels_of(s0 + lane));
+        level = __reduce_max_sync(0xffffffffu, level) - 1;
+        int here = level >= 0 ? count(level) : 0;         // sequences with this level
+        long long base = 0;                               // items before it
+        const int P = gridDim.x;
+        int k = 0, F = 0;     // items published, tiles loaded
+        bool ok = true;
+        for (long long turn = 0; ok; ++turn) {
+            const long long rank = turn * P + (turn & 1 ? P - 1 - blockIdx.x : blockIdx.x);
+            while (level >= 0 && rank >= base + (long long)here * per_seq) {
+                base += (long long)here * per_seq;
+                --level;
+                here = level >= 0 ? count(level) : 0;
+            }
+            PromptItem it;
+            it.row0 = it.len = it.kvh = it.tiles = 0;
+            for (int u = 0; u < 2; ++u) it.blk[u] = it.head[u] = it.n[u] = 0;
+            if (level >= 0) {
+                int nth = (int)((rank - base) / per_seq);
+                const int rem = (int)((rank - base) % per_seq);
+                it.kvh = rem % a.nkv;
+                for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
+                    const unsigned m = __ballot_sync(0xffffffffu, levels_of(s0 + lane) > level);
+                    if (nth < __popc(m)) {
+                        const int src = __fns(m, 0, nth + 1);
+                        it.row0 = __shfl_sync(0xffffffffu, row0, src);
+                        it.len = __shfl_sync(0xffffffffu, len, src);
+                        break;
+                    }
+                    nth -= __popc(m);
+                }
+                const int blocks = (it.len + kTile - 1) / kTile;
+                for (int u = 0; u < 2; ++u) {
+                    const int unit = rem / a.nkv * 2 + u, blk = level * R + unit / G;
+                    if (blk >= blocks) break;
+                    it.blk[u] = blk;
+                    it.head[u] = it.kvh * G + unit % G;
+                    it.n[u] = blk + 1;
+                    it.tiles = blk + 1;
+                }
+                if (it.n[0] == 0) continue;      // a lone last row block has half the units
+                if (it.n[1] == 0) it.blk[1] = it.blk[0];
+            }
+            const int slot = k & 1;
+            if (k >= 2) ok = mbar_wait_warp(&t.item_empty[slot], ((k >> 1) - 1) & 1, &t.abort);
+            if (!ok) break;
+            if (lane == 0) {
+                t.item[slot] = it;
+                mbar_arrive(&t.item_full[slot]);
+            }
+            if (level < 0) break;
+            if (k > 0) ok = mbar_wait_warp(&t.q_empty, (k - 1) & 1, &t.abort);
+            if (!ok) break;
+            ++k;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&t.q_full, (it.n[1] ? 2 : 1) * L::kTileBytes);
                 for (int h = 0; h < D / 64; ++h)
-                    tma_load_3d(smem + L::kRing + st * L::kTileBytes + h * kTile * 128, f & 1 ? &p.v : &p.k, h * 64,
-                                kvh, row0 + (f >> 1) * kTile, &t.full[st]);
+                    for (int u = 0; u < (it.n[1] ? 2 : 1); ++u)
+                        tma_load_3d(smem + L::kQ + u * L::kTileBytes + h * kTile * 128, &p.q, h * 64, it.head[u],
+                                    it.row0 + it.blk[u] * kTile, &t.q_full);
             }
-            // every tile used: nothing is in flight when the block ends
-            for (int st = 0; st < L::kStages && ok; ++st) {
-                const int uses = (2 * J - st + L::kStages - 1) / L::kStages;
-                if (uses > 0) ok = mbar_wait(&t.empty[st], (uses - 1) & 1, &t.abort);
+            for (int f = 0; f < 2 * it.tiles && ok; ++f, ++F) {       // K0 V0 K1 V1 ...
+                const int st = F % L::kStages, use = F / L::kStages;
+                if (use > 0) ok = mbar_wait_warp(&t.empty[st], (use - 1) & 1, &t.abort);
+                if (ok && lane == 0) {
+                    mbar_arrive_expect_tx(&t.full[st], L::kTileBytes);
+                    for (int h = 0; h < D / 64; ++h)
+                        tma_load_3d(smem + L::kRing + st * L::kTileBytes + h * kTile * 128, f & 1 ? &p.v : &p.k, h * 64,
+                                    it.kvh, it.row0 + (f >> 1) * kTile, &t.full[st]);
+                }
             }
+        }
+        // every tile used: nothing is in flight when the block ends
+        for (int st = 0; st < L::kStages && ok; ++st) {
+            const int uses = (F - st + L::kStages - 1) / L::kStages;
+            if (uses > 0) ok = mbar_wait_warp(&t.empty[st], (uses - 1) & 1, &t.abort);
         }
     } else if (warp == 9) {
         // ---- MMA issuer: the whole warp walks the loop (addresses stay
@@ -248,45 +308,81 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
         auto full = [&](int f) {
             return mbar_wait_warp(&t.full[f % L::kStages], (f / L::kStages) & 1, &t.abort);
         };
-        bool ok = mbar_wait_warp(&t.q_full, 0, &t.abort) && full(0);
-        if (ok) {
-            qk(0, 0);
-            if (two) qk(1, 0);
-            if (leader) tc_commit(&t.empty[0]);
-        }
-        for (int j = 0; j < J && ok; ++j) {
-            const int fv = 2 * j + 1, fk = 2 * j + 2;
-            ok = full(fv);
+        int F = 0, tiles[2] = {0, 0}, outs[2] = {0, 0}, masked[2] = {0, 0};    // phases so far
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            ok = mbar_wait_warp(&t.item_full[k & 1], (k >> 1) & 1, &t.abort);
             if (!ok) break;
-            if (j >= blk0 && leader) mbar_arrive(&t.guard_go[j - blk0]);   // a masked tile (the last, or last two)
+            const PromptItem &it = t.item[k & 1];
+            const int J = __shfl_sync(0xffffffffu, it.tiles, 0), blk0 = __shfl_sync(0xffffffffu, it.blk[0], 0);
+            const int n0 = __shfl_sync(0xffffffffu, it.n[0], 0), n1 = __shfl_sync(0xffffffffu, it.n[1], 0);
+            __syncwarp();
+            if (J == 0) break;
+            if (leader) mbar_arrive(&t.item_empty[k & 1]);
+            ok = mbar_wait_warp(&t.q_full, k & 1, &t.abort) && full(F);
+            if (!ok) break;
+            qk(0, F);
+            if (n1) qk(1, F);
+            if (leader) {
+                tc_commit(&t.empty[F % L::kStages]);
+                if (J == 1) tc_commit(&t.q_empty);
+            }
+            for (int j = 0; j < J && ok; ++j) {
+                const int fv = F + 2 * j + 1, fk = F + 2 * j + 2;
+                ok = full(fv);
+                if (!ok) break;
+                const bool mask = j >= blk0;      // the last tile, or the last two
+                if (mask && leader) mbar_arrive(&t.guard_go[j - blk0]);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int n = u ? n1 : n0;
-                if (j >= n || !ok) continue;
-                ok = mbar_wait_warp(&t.p_ready[u], j & 1, &t.abort);
-                if (ok && j >= blk0) ok = mbar_wait_warp(&t.guard_done[j - blk0], 0, &t.abort);
-                if (!ok) continue;
-                tc_fence_after();
-                pv(u, fv, j == 0, j + 1 == n);
-                if (j + 1 < n) {
-                    ok = full(fk);
-                    if (ok) qk(u, fk);
+                for (int u = 0; u < 2; ++u) {
+                    const int n = u ? n1 : n0;
+                    if (j >= n || !ok) continue;
+                    ok = mbar_wait_warp(&t.p_ready[u], tiles[u]++ & 1, &t.abort);
+                    if (ok && j == 0 && outs[u] > 0) ok = mbar_wait_warp(&t.o_empty[u], (outs[u] - 1) & 1, &t.abort);
+                    if (ok && mask)
+                        ok = mbar_wait_warp(&t.guard_done[j - blk0], (j == blk0 ? masked[0] : masked[1]) & 1, &t.abort);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    pv(u, fv, j == 0, j + 1 == n);
+                    if (j + 1 < n) {
+                        ok = full(fk);
+                        if (ok) qk(u, fk);
+                    }
+                }
+                if (ok && leader) {
+                    tc_commit(&t.empty[fv % L::kStages]);
+                    if (j + 1 < J) tc_commit(&t.empty[fk % L::kStages]);
+                    if (j + 2 == J) tc_commit(&t.q_empty);      // the queries' last product
                 }
             }
-            if (ok && leader) {
-                tc_commit(&t.empty[fv % L::kStages]);
-                if (j + 1 < J) tc_commit(&t.empty[fk % L::kStages]);
-            }
+            ++masked[0];
+            if (J - 1 > blk0) ++masked[1];
+            ++outs[0];
+            if (n1) ++outs[1];
+            F += 2 * J;
         }
     } else if (warp >= 10) {
         // ---- guard of the masked tiles
         const int gt = tid - 10 * 32;
+        int F = 0, masked[2] = {0, 0};
         bool ok = true;
-        for (int which = 0; which < (blk1 != blk0 ? 2 : 1) && ok; ++which) {
+        for (int k = 0; ok; ++k) {
+            const int slot = k & 1;
+            ok = mbar_wait_warp(&t.item_full[slot], (k >> 1) & 1, &t.abort);
+            if (!ok) break;
+            const int J = t.item[slot].tiles, blk0 = t.item[slot].blk[0], len = t.item[slot].len;
+            if (J == 0) break;
+            if (t.any[slot]) {       // what the item before last left here
+                for (int i = gt; i < 3 * 128; i += 64) (&t.first[slot][0][0])[i] = 0x7fffffff;
+                asm volatile("bar.sync 1, 64;" ::: "memory");
+                if (gt == 0) t.any[slot] = 0;
+                asm volatile("bar.sync 1, 64;" ::: "memory");
+            }
+            for (int which = 0; which < J - blk0 && ok; ++which) {
             // the issuer says when the tile is there: a wait on the tile's own
             // barrier from here could miss phases of the tiles before it
-            const int j = blk0 + which, f = 2 * j + 1;
-            ok = mbar_wait_warp(&t.guard_go[which], 0, &t.abort) &&
+            const int j = blk0 + which, f = F + 2 * j + 1;
+            ok = mbar_wait_warp(&t.guard_go[which], masked[which]++ & 1, &t.abort) &&
                  mbar_wait_warp(&t.full[f % L::kStages], (f / L::kStages) & 1, &t.abort);
             if (!ok) break;
             uint4 *tile = reinterpret_cast<uint4 *>(smem + L::kRing + f % L::kStages * L::kTileBytes);
@@ -308,29 +404,37 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                         const int col = half * 64 + ((i ^ r) & 7) * 8 + c;
                         if (j * kTile + r < len) {
                             const int kind = (w & ~kExp & 0x7fffu) ? 0 : w & 0x8000u ? 2 : 1;
-                            atomicMin(&t.first[kind][col], j * kTile + r);
-                            t.any = 1;
+                            atomicMin(&t.first[slot][kind][col], j * kTile + r);
+                            t.any[slot] = 1;
                         }
                     }
                 fence_async_smem();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&t.guard_done[which]);
+            }
+            if (lane == 0) mbar_arrive(&t.item_empty[slot]);
+            F += 2 * J;
         }
     } else {
         // ---- softmax: one row per thread
         set_regs_up<kSoftmaxRegs>();
         const int u = warp >> 2, r = tid & 127;
-        const int n = u ? n1 : n0, blk = u ? blk1 : blk0, head = u ? head1 : head0;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // lane 32 (w % 4) in bits 16..
         const uint32_t ts = tmem + u * kTile + lanes, to = tmem + 2 * kTile + u * D + lanes;
         const float c = a.scale * 1.4426950408889634f;
-        float m = -INFINITY, l = 0.f;
+        int tiles = 0, outs = 0;      // phases so far
         bool ok = true;
+        for (int k = 0; ok; ++k) {
+        const int slot = k & 1;
+        ok = mbar_wait_warp(&t.item_full[slot], (k >> 1) & 1, &t.abort);
+        if (!ok || t.item[slot].tiles == 0) break;
+        const int n = t.item[slot].n[u], blk = t.item[slot].blk[u];
+        float m = -INFINITY, l = 0.f;
         for (int j = 0; j < n && ok; ++j) {
             // S of this tile; the products of the tile before are done too (one
             // thread issues all of them, in this order)
-            ok = mbar_wait_warp(&t.s_full[u], j & 1, &t.abort);
+            ok = mbar_wait_warp(&t.s_full[u], tiles++ & 1, &t.abort);
             if (!ok) break;
             tc_fence_after();
             uint32_t x[4][32];
@@ -406,25 +510,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
             l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
             if (top != top) l = NAN;      // a score that is not a number
         }
-        if (ok && n > 0) ok = mbar_wait_warp(&t.o_full[u], 0, &t.abort);
+        if (ok && n > 0) ok = mbar_wait_warp(&t.o_full[u], outs++ & 1, &t.abort);
         if (ok && n > 0) {
             tc_fence_after();
-            const int pos = blk * kTile + r;
+            const int pos = blk * kTile + r, len = t.item[slot].len;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            uint16_t *dst = (uint16_t *)a.out + (long long)(row0 + pos) * a.out_stride + (long long)head * D;
-            const bool any = t.any != 0;
+            uint16_t *dst = (uint16_t *)a.out + (long long)(t.item[slot].row0 + pos) * a.out_stride +
+                            (long long)t.item[slot].head[u] * D;
+            const bool any = t.any[slot] != 0;
+#pragma unroll
             for (int q = 0; q < D / 32; ++q) {
                 uint32_t x[32];
                 tmem_ld32(to + q * 32, x);
                 tmem_ld_wait();
+                if (q == D / 32 - 1) {      // O is read: the next item may start its own
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&t.o_empty[u]);
+                }
                 if (any)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const int col = q * 32 + i;
                         float o = __uint_as_float(x[i]);
-                        if (t.first[0][col] <= pos) o = NAN;
-                        if (t.first[1][col] <= pos) o += INFINITY;
-                        if (t.first[2][col] <= pos) o -= INFINITY;
+                        if (t.first[slot][0][col] <= pos) o = NAN;
+                        if (t.first[slot][1][col] <= pos) o += INFINITY;
+                        if (t.first[slot][2][col] <= pos) o -= INFINITY;
                         x[i] = __float_as_uint(o);
                     }
                 if (pos < len)
@@ -438,6 +549,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                         *reinterpret_cast<uint4 *>(dst + q * 32 + i) = w;
                     }
             }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&t.item_empty[slot]);
         }
     }
 
@@ -506,21 +620,23 @@ cudaError_t launch(const PromptParams &p, int device, int grid, cudaStream_t str
 
 }  // namespace
 
-cudaError_t prompt_launch(const PromptArgs &a, int device, int, cudaStream_t stream) {
+cudaError_t prompt_launch(const PromptArgs &a, int device, int num_sms, cudaStream_t stream) {
     PromptParams p;
     p.a = a;
     if (!make_map(&p.q, a.dtype, a.q, a.d, a.nq, a.n_tokens, a.q_stride) ||
         !make_map(&p.k, a.dtype, a.k, a.d, a.nkv, a.n_tokens, a.k_stride) ||
         !make_map(&p.v, a.dtype, a.v, a.d, a.nkv, a.n_tokens, a.v_stride))
         return cudaErrorInvalidValue;
-    // at most this many items: a sequence of n row blocks has ceil(n G / 2) per KV head
-    const long long G = a.nq / a.nkv, top = a.max_len < a.n_tokens ? a.max_len : a.n_tokens;
+    // one block per SM, fewer where there are fewer items: row blocks (at most
+    // n_tokens / 128 and one more per sequence, or what max_len allows) times
+    // half the heads, rounded up for an odd group
+    const long long top = a.max_len < a.n_tokens ? a.max_len : a.n_tokens;
     long long blocks = a.n_tokens / kTile + a.n_seqs;
     const long long most = a.n_seqs * ((top + kTile - 1) / kTile);
     if (most < blocks) blocks = most;
-    long long grid = (blocks * G + a.n_seqs + 1) / 2 * a.nkv;
+    long long grid = blocks * ((a.nq / a.nkv + 1) / 2) * a.nkv;
     if (grid < 1) grid = 1;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (grid > num_sms) grid = num_sms;
     if (a.dtype == MK_BF16)
         return a.d == 64 ? launch<Bf16, 64>(p, device, (int)grid, stream)
                          : launch<Bf16, 128>(p, device, (int)grid, stream);
