@@ -29,7 +29,9 @@
 // shared memory and remembered per column with their first key; the epilogue
 // adds them to the rows that do see them.
 //
-// Tensor memory: S0 | S1 | O0 | O1 (P overwrites the first half of its S).
+// Tensor memory, 512 columns: S0 | S1 | O0 | O1, and for 64 dims P0 | P1: the
+// next tile's S is then computed while this one's softmax runs.  For 128 dims
+// P lies over the first half of its S.
 #include <cuda.h>
 
 #include <atomic>
@@ -61,10 +63,8 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 }
 // 2^x of a pair by multiplications and additions, for x <= 127 (results below
 // 2^-126 are given as 2^-126; not for NaN): the nearest integer by adding
-// 1.5 * 2^23, and a polynomial for the rest in [-1/2, 1/2] whose relative
-// error is least at its degree (3: 7.5e-5, for weights rounded to bf16; 4:
-// 2.6e-6, for fp16).
-template <int DEG>
+// 1.5 * 2^23, and for the rest in [-1/2, 1/2] the cubic of least relative error
+// (7.5e-5, below the rounding of the weights to 16 bits).
 __device__ __forceinline__ float2 ex2_fma(float2 x) {
     x.x = fmaxf(x.x, -126.f);
     x.y = fmaxf(x.y, -126.f);
@@ -72,17 +72,9 @@ __device__ __forceinline__ float2 ex2_fma(float2 x) {
     const float2 n = fadd2(x, two(12582912.f));
     const float2 f = fadd2(n, two(-12582912.f));
     const float2 r = ffma2(f, two(-1.f), x);
-    float2 p;
-    if constexpr (DEG == 3) {
-        p = ffma2(r, two(0.0551716685295105f), two(0.2426111251115799f));
-        p = ffma2(r, p, two(0.6932609677314758f));
-        p = ffma2(r, p, two(0.9999280571937561f));
-    } else {
-        p = ffma2(r, two(0.009570102207362652f), two(0.05591785907745361f));
-        p = ffma2(r, p, two(0.240247443318367f));
-        p = ffma2(r, p, two(0.6931217908859253f));
-        p = ffma2(r, p, two(0.9999992847442627f));
-    }
+    float2 p = ffma2(r, two(0.0551716685295105f), two(0.2426111251115799f));
+    p = ffma2(r, p, two(0.6932609677314758f));
+    p = ffma2(r, p, two(0.9999280571937561f));
     return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(n.x) << 23)),
                        __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(n.y) << 23)));
 }
@@ -94,7 +86,8 @@ struct PromptSmem {
     static constexpr int kQ = 0;
     static constexpr int kRing = 2 * kTileBytes;
     static constexpr int kTail = kRing + kStages * kTileBytes;
-    static constexpr int kBytes = kTail + 4096 + 1024;   // barriers, items; slack to align the base
+    static constexpr int kStore = kTail + 4096;          // 2 KB a softmax warp: 32 rows of 32 output columns
+    static constexpr int kBytes = kStore + 8 * 2048;
 };
 
 struct PromptItem {
@@ -107,7 +100,7 @@ struct PromptItem {
 struct PromptTail {
     uint64_t full[8], empty[8];               // the ring of K and V tiles
     uint64_t q_full, q_empty;                 // both units' queries
-    uint64_t s_full[2], p_ready[2];           // per tile
+    uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2];   // per tile
     uint64_t o_full[2], o_empty[2];           // per item
     uint64_t guard_go[2], guard_done[2];      // the first and second masked tile of an item
     uint64_t item_full[2], item_empty[2];
@@ -128,8 +121,7 @@ template <class T, int D>
 __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __grid_constant__ PromptParams p) {
     using L = PromptSmem<D>;
     constexpr bool kBf16 = T::kBf16;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *smem = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) unsigned char smem[];
     PromptTail &t = *reinterpret_cast<PromptTail *>(smem + L::kTail);
     const PromptArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -151,7 +143,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
             mbar_init(&t.q_empty, 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&t.s_full[i], 1);
+                mbar_init(&t.s_free[i], 4);
                 mbar_init(&t.p_ready[i], 4);
+                mbar_init(&t.pv_done[i], 1);
                 mbar_init(&t.o_full[i], 1);
                 mbar_init(&t.o_empty[i], 4);
                 mbar_init(&t.guard_go[i], 1);
@@ -283,6 +277,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
         const uint32_t ring = (smem_addr(smem + L::kRing) & 0x3FFFFu) >> 4, qs = (smem_addr(smem + L::kQ) & 0x3FFFFu) >> 4;
         constexpr uint32_t kIdS = f16_idesc(kBf16, false, kTile, kTile);
         constexpr uint32_t kIdO = f16_idesc(kBf16, true, kTile, D);
+        constexpr bool kOwnP = D == 64;
         auto qk = [&](int u, int f) {
             const uint32_t kb = ring + (f % L::kStages) * (L::kTileBytes >> 4), qb = qs + u * (L::kTileBytes >> 4);
             if (leader) {
@@ -297,18 +292,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
         };
         auto pv = [&](int u, int f, bool first, bool last) {
             const uint32_t vb = ring + (f % L::kStages) * (L::kTileBytes >> 4);
+            const uint32_t pb = tmem + (kOwnP ? 2 * kTile + 2 * D + u * 64 : u * kTile);
             if (leader) {
 #pragma unroll
                 for (int s = 0; s < kTile / 16; ++s)
-                    mma_ts(tmem + 2 * kTile + u * D, tmem + u * kTile + s * 8,
+                    mma_ts(tmem + 2 * kTile + u * D, pb + s * 8,
                            desc_sw128_at(vb + (s * 16 * 128 >> 4), kTile * 128, 1024), kIdO, s > 0 || !first);
+                if (kOwnP) tc_commit(&t.pv_done[u]);
                 if (last) tc_commit(&t.o_full[u]);
             }
         };
         auto full = [&](int f) {
             return mbar_wait_warp(&t.full[f % L::kStages], (f / L::kStages) & 1, &t.abort);
         };
-        int F = 0, tiles[2] = {0, 0}, outs[2] = {0, 0}, masked[2] = {0, 0};    // phases so far
+        int F = 0, products[2] = {0, 0}, tiles[2] = {0, 0}, outs[2] = {0, 0}, masked[2] = {0, 0};    // phases so far
         bool ok = true;
         for (int k = 0; ok; ++k) {
             ok = mbar_wait_warp(&t.item_full[k & 1], (k >> 1) & 1, &t.abort);
@@ -319,20 +316,38 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
             __syncwarp();
             if (J == 0) break;
             if (leader) mbar_arrive(&t.item_empty[k & 1]);
-            ok = mbar_wait_warp(&t.q_full, k & 1, &t.abort) && full(F);
-            if (!ok) break;
-            qk(0, F);
-            if (n1) qk(1, F);
-            if (leader) {
-                tc_commit(&t.empty[F % L::kStages]);
-                if (J == 1) tc_commit(&t.q_empty);
-            }
+            ok = mbar_wait_warp(&t.q_full, k & 1, &t.abort);
+            // S of the units that have tile j
+            auto both_qk = [&](int j) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (j >= (u ? n1 : n0) || !ok) continue;
+                    if (kOwnP) {
+                        if (products[u] > 0) ok = mbar_wait_warp(&t.s_free[u], (products[u] - 1) & 1, &t.abort);
+                        ++products[u];
+                        tc_fence_after();
+                    }
+                    if (ok) ok = full(F + 2 * j);
+                    if (ok) qk(u, F + 2 * j);
+                }
+            };
+            auto qk_used = [&](int j) {       // tile j's keys, and with the last one the queries
+                if (!ok || !leader) return;
+                tc_commit(&t.empty[(F + 2 * j) % L::kStages]);
+                if (j + 1 == J) tc_commit(&t.q_empty);
+            };
+            if (ok) both_qk(0);
+            qk_used(0);
             for (int j = 0; j < J && ok; ++j) {
-                const int fv = F + 2 * j + 1, fk = F + 2 * j + 2;
+                const int fv = F + 2 * j + 1;
                 ok = full(fv);
                 if (!ok) break;
                 const bool mask = j >= blk0;      // the last tile, or the last two
                 if (mask && leader) mbar_arrive(&t.guard_go[j - blk0]);
+                if (kOwnP && j + 1 < J) {
+                    both_qk(j + 1);
+                    qk_used(j + 1);
+                }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int n = u ? n1 : n0;
@@ -344,16 +359,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                     if (!ok) continue;
                     tc_fence_after();
                     pv(u, fv, j == 0, j + 1 == n);
-                    if (j + 1 < n) {
-                        ok = full(fk);
-                        if (ok) qk(u, fk);
+                    if (!kOwnP && j + 1 < n) {
+                        ok = full(fv + 1);
+                        if (ok) qk(u, fv + 1);
                     }
                 }
-                if (ok && leader) {
-                    tc_commit(&t.empty[fv % L::kStages]);
-                    if (j + 1 < J) tc_commit(&t.empty[fk % L::kStages]);
-                    if (j + 2 == J) tc_commit(&t.q_empty);      // the queries' last product
-                }
+                if (ok && leader) tc_commit(&t.empty[fv % L::kStages]);
+                if (!kOwnP && j + 1 < J) qk_used(j + 1);
             }
             ++masked[0];
             if (J - 1 > blk0) ++masked[1];
@@ -422,8 +434,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
         const int u = warp >> 2, r = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // lane 32 (w % 4) in bits 16..
         const uint32_t ts = tmem + u * kTile + lanes, to = tmem + 2 * kTile + u * D + lanes;
+        constexpr bool kOwnP = D == 64;
+        const uint32_t tp = kOwnP ? tmem + 2 * kTile + 2 * D + u * 64 + lanes : ts;
         const float c = a.scale * 1.4426950408889634f;
-        int tiles = 0, outs = 0;      // phases so far
+        int tiles = 0, outs = 0, pvs = 0;      // phases so far
         bool ok = true;
         for (int k = 0; ok; ++k) {
         const int slot = k & 1;
@@ -432,8 +446,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
         const int n = t.item[slot].n[u], blk = t.item[slot].blk[u];
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < n && ok; ++j) {
-            // S of this tile; the products of the tile before are done too (one
-            // thread issues all of them, in this order)
+            // S of this tile (for 128 dims the products of the tile before are
+            // done too: one thread issues all of them, in this order)
             ok = mbar_wait_warp(&t.s_full[u], tiles++ & 1, &t.abort);
             if (!ok) break;
             tc_fence_after();
@@ -441,6 +455,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, x[q]);
             tmem_ld_wait();
+            if constexpr (kOwnP) {      // S is read: the next tile's may be computed
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&t.s_free[u]);
+            }
             if (j == blk)      // the diagonal: keys beyond the row's own are not seen
 #pragma unroll
                 for (int i = 0; i < kTile; ++i)
@@ -459,9 +478,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
             const float old = m;
             if (!((top - m) * c <= kRescale)) m = fmaxf(m, top);
             const bool raise = m != old;
+            // P and O are free once the tile before is weighted (128 dims: it is)
+            auto weighted = [&] {
+                if (!kOwnP || j == 0) return true;
+                const bool done = mbar_wait_warp(&t.pv_done[u], pvs & 1, &t.abort);
+                tc_fence_after();
+                return done;
+            };
             if (__any_sync(0xffffffffu, raise)) {
                 const float f = raise ? ex2((old - m) * c) : 1.f;
                 l *= f;
+                ok = weighted();
+                if (!ok) break;
                 if (j > 0)
 #pragma unroll 1
                     for (int q = 0; q < D / 16; ++q) {
@@ -485,7 +513,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                         float2 e0 = ffma2(make_float2(at(q * 32 + i), at(q * 32 + i + 1)), c2, mc2);
                         float2 e1 = ffma2(make_float2(at(q * 32 + i + 2), at(q * 32 + i + 3)), c2, mc2);
                         if (mixed.value && (i / 4) % kPolyOf < kPolyNum) {
-                            e0 = ex2_fma<kBf16 ? 3 : 4>(e0);
+                            e0 = ex2_fma(e0);
                         } else {
                             e0.x = ex2(e0.x);
                             e0.y = ex2(e0.y);
@@ -497,12 +525,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                         w[i / 2] = T::pack(e0.x, e0.y);
                         w[i / 2 + 1] = T::pack(e1.x, e1.y);
                     }
-                    tmem_st16(ts + q * 16, w);      // P, over what this row has read of S
+                    if (q == 0) ok = weighted();
+                    tmem_st16(tp + q * 16, w);      // (128 dims: over what this row has read of S)
                 }
             };
             // masked scores have to give exactly zero: the function unit alone
             if (j == blk) weights(std::false_type());
             else weights(std::true_type());
+            if (!ok) break;
+            if (kOwnP && j > 0) ++pvs;
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -510,12 +541,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
             l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
             if (top != top) l = NAN;      // a score that is not a number
         }
+        if (kOwnP && ok && n > 0) ok = mbar_wait_warp(&t.pv_done[u], pvs++ & 1, &t.abort);
         if (ok && n > 0) ok = mbar_wait_warp(&t.o_full[u], outs++ & 1, &t.abort);
         if (ok && n > 0) {
             tc_fence_after();
             const int pos = blk * kTile + r, len = t.item[slot].len;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            uint16_t *dst = (uint16_t *)a.out + (long long)(t.item[slot].row0 + pos) * a.out_stride +
+            // rows leave through shared memory, eight rows of 64 bytes a store:
+            // one row a thread took 32 transactions a store instruction (the
+            // epilogue 7400 cycles at 128 dims)
+            uint4 *stage = reinterpret_cast<uint4 *>(smem + L::kStore + warp * 2048);
+            auto staged = [&](int row, int chunk) { return stage + row * 4 + (chunk ^ (row >> 1 & 3)); };
+            const int row_first = blk * kTile + (warp & 3) * 32;
+            uint16_t *dst = (uint16_t *)a.out + (long long)(t.item[slot].row0 + row_first) * a.out_stride +
                             (long long)t.item[slot].head[u] * D;
             const bool any = t.any[slot] != 0;
 #pragma unroll
@@ -538,16 +576,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                         if (t.first[slot][2][col] <= pos) o -= INFINITY;
                         x[i] = __float_as_uint(o);
                     }
-                if (pos < len)
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint4 w;
-                        w.x = T::pack(__uint_as_float(x[i]) * inv, __uint_as_float(x[i + 1]) * inv);
-                        w.y = T::pack(__uint_as_float(x[i + 2]) * inv, __uint_as_float(x[i + 3]) * inv);
-                        w.z = T::pack(__uint_as_float(x[i + 4]) * inv, __uint_as_float(x[i + 5]) * inv);
-                        w.w = T::pack(__uint_as_float(x[i + 6]) * inv, __uint_as_float(x[i + 7]) * inv);
-                        *reinterpret_cast<uint4 *>(dst + q * 32 + i) = w;
-                    }
+                for (int i = 0; i < 32; i += 8) {
+                    uint4 w;
+                    w.x = T::pack(__uint_as_float(x[i]) * inv, __uint_as_float(x[i + 1]) * inv);
+                    w.y = T::pack(__uint_as_float(x[i + 2]) * inv, __uint_as_float(x[i + 3]) * inv);
+                    w.z = T::pack(__uint_as_float(x[i + 4]) * inv, __uint_as_float(x[i + 5]) * inv);
+                    w.w = T::pack(__uint_as_float(x[i + 6]) * inv, __uint_as_float(x[i + 7]) * inv);
+                    *staged(lane, i / 8) = w;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = i * 8 + (lane >> 2), chunk = lane & 3;
+                    if (row_first + row < len)
+                        *reinterpret_cast<uint4 *>(dst + row * a.out_stride + q * 32 + chunk * 8) = *staged(row, chunk);
+                }
+                __syncwarp();
             }
         }
         __syncwarp();
