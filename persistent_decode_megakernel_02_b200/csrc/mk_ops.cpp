@@ -102,7 +102,7 @@ int mk_kv_append(const mk_paged_kv *kv, const int32_t *cu_tokens, const int32_t 
     if (st != MK_OK) return st;
     AppendArgs a{*kv, cu_tokens, start_pos, n_tokens, n_q_heads, q, k, v, q_stride, k_stride, v_stride, rope_theta,
                  q_out, k_out, q_out_stride, k_out_stride, status_out};
-    return launched(append_launch(a, (cudaStream_t)stream));
+    return launched(append_launch(a, sms, (cudaStream_t)stream));
 }
 
 int mk_paged_attention_workspace(const mk_paged_kv *kv, int max_len, int n_q_heads, size_t *bytes_out) {

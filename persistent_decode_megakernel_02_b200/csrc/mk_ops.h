@@ -25,7 +25,7 @@ struct AppendArgs {
     long long q_out_stride, k_out_stride;
     int32_t *status;
 };
-cudaError_t append_launch(const AppendArgs &a, cudaStream_t stream);
+cudaError_t append_launch(const AppendArgs &a, int num_sms, cudaStream_t stream);
 
 struct PagedArgs {
     mk_paged_kv kv;
