@@ -1,4 +1,5 @@
-"""Build libmk.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build libmk.so (the C-ABI library) in-tree with nvcc for sm_100a, and the
+binding's compiled fast path (_mk_fast.so) with g++ against torch's headers.
 
     python -m persistent_decode_megakernel_02_b200.build [--verbose]
 """
@@ -43,27 +44,62 @@ def _digest() -> str:
     return h.hexdigest()
 
 
-def _stale() -> bool:
+def _stale(lib: str = LIB, digest=None) -> bool:
     # content-based: copies of the tree (which may not keep mtimes) reuse the
     # library as long as its inputs are unchanged
-    if not os.path.exists(LIB) or not os.path.exists(STAMP):
+    stamp = lib + ".sha256"
+    if not os.path.exists(lib) or not os.path.exists(stamp):
         return True
-    with open(STAMP) as f:
-        return f.read().strip() != _digest()
+    with open(stamp) as f:
+        return f.read().strip() != (digest or _digest)()
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
-    cmd = [_nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC", "-shared",
-           "-I", os.path.join(ROOT, "include"), "-o", LIB]
-    if verbose:
-        cmd += ["-Xptxas", "-v"]
-    cmd += [os.path.join(CSRC, f) for f in SOURCES]
-    subprocess.check_call(cmd)
-    with open(STAMP, "w") as f:
-        f.write(_digest())
+    if force or _stale():
+        cmd = [_nvcc(), "-O3", "-std=c++17", *ARCH, "-t", "0", "-lineinfo", "-Xcompiler", "-fPIC", "-shared",
+               "-I", os.path.join(ROOT, "include"), "-o", LIB]
+        if verbose:
+            cmd += ["-Xptxas", "-v"]
+        cmd += [os.path.join(CSRC, f) for f in SOURCES]
+        subprocess.check_call(cmd)
+        with open(STAMP, "w") as f:
+            f.write(_digest())
+    build_fast(force)
     return LIB
+
+
+FAST = os.path.join(HERE, "_mk_fast.so")
+FAST_SOURCE = os.path.join(CSRC, "mk_fast.cpp")
+
+
+def _fast_digest() -> str:
+    """Hash of the fast path's source, the header and the versions it binds to."""
+    import hashlib
+    import torch
+    h = hashlib.sha256(f"{torch.__version__} {sys.version}".encode())
+    for f in (FAST_SOURCE, os.path.join(ROOT, "include", "mk.h")):
+        with open(f, "rb") as fh:
+            h.update(fh.read())
+    return h.hexdigest()
+
+
+def build_fast(force: bool = False) -> str:
+    if not force and not _stale(FAST, _fast_digest):
+        return FAST
+    import sysconfig
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.isabs(_nvcc()) else "/usr/local/cuda"
+    subprocess.check_call(
+        ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         "-isystem", os.path.join(base, "include"),
+         "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+         "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+         "-I", os.path.join(ROOT, "include"), "-o", FAST, FAST_SOURCE, "-L", HERE, "-lmk",
+         "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
+    with open(FAST + ".sha256", "w") as f:
+        f.write(_fast_digest())
+    return FAST
 
 
 if __name__ == "__main__":

@@ -1,8 +1,11 @@
 """Thin ctypes binding of libmk.so (include/mk.h).
 
 Argument marshalling only: every step of the decode path runs in the CUDA
-library.  Torch tensors are used for device memory and streams.  If the
-library is missing this module raises at import time: there is no fallback.
+library.  Torch tensors are used for device memory and streams.  The serving
+operators go through _mk_fast (the same checks and calls, compiled) where the
+call is the plain one, and through ctypes otherwise.  If the library or the
+compiled module is missing this module raises at import time: there is no
+fallback.
 """
 from __future__ import annotations
 
@@ -35,6 +38,8 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with "
                       "`python -m persistent_decode_megakernel_02_b200.build`")
 _lib = C.CDLL(LIB_PATH)
+import torch  # noqa: E402  (before _mk_fast, which links against it)
+from . import _mk_fast as _fast  # noqa: E402
 
 
 class MkError(RuntimeError):
@@ -384,14 +389,15 @@ class Context:
 # Each checks its tensors (device, type, layout) here, because the library
 # sees pointers only; what it finds wrong is an MkError of MK_ERR_INVALID, as
 # are the library's own refusals.  The tensors' device is made current for
-# the call; stream=None means that device's current stream.
+# the call; stream=None means that device's current stream.  _fast makes the
+# call and returns 0 if all is well and the device is current; whatever else it
+# returns, the way below it checks again and says what is wrong.
 
 def _invalid(what: str, why: str):
     raise MkError(MK_ERR_INVALID, f"{what}: {why}")
 
 
 def _dtype_code(dtype) -> int:
-    import torch
     return MK_BF16 if dtype is torch.bfloat16 else MK_FP16 if dtype is torch.float16 else -1
 
 
@@ -421,7 +427,6 @@ def _vec(what: str, name: str, t, dtype, dev: int, n: int):
 def _launch(what: str, fn, dev: int, stream, args: tuple):
     """Call `fn(*args, stream)` with device `dev` current, on `stream` or the
     device's current stream."""
-    import torch
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(dev)
     else:
@@ -443,7 +448,6 @@ class PagedKV:
     int32 [n_seqs][pages_per_seq].  Holds the tensors it names."""
 
     def __init__(self, k, v, page_table):
-        import torch
         what = "PagedKV"
         if k.dim() != 4 or _dtype_code(k.dtype) < 0 or not k.is_cuda or not k.is_contiguous():
             _invalid(what, "k must be a contiguous bf16 or fp16 CUDA tensor "
@@ -461,6 +465,7 @@ class PagedKV:
                                  self.num_pages, self.page_size, self.n_kv_heads, self.head_dim,
                                  _dtype_code(k.dtype))
         self._ref = C.byref(self._st)
+        self._addr = C.addressof(self._st)
 
 
 def kv_append(cache: PagedKV, q, k, v, cu_tokens, start_pos, rope_theta: float, q_out=None, k_out=None,
@@ -469,7 +474,9 @@ def kv_append(cache: PagedKV, q, k, v, cu_tokens, start_pos, rope_theta: float, 
     (or None: k only), k, v [n][n_kv_heads][d], cu_tokens int32 [n_seqs + 1],
     start_pos int32 [n_seqs].  q_out (default: in place) receives the rotated
     q, k_out (default: not kept) the rotated k as rows."""
-    import torch
+    if stream is None and not _fast.kv_append(cache._addr, cache.dev, q, k, v, cu_tokens, start_pos, rope_theta, q_out,
+                                              k_out, status):
+        return
     what, dev, dt, i32 = "kv_append", cache.dev, cache.dtype, torch.int32
     n = k.shape[0] if k.dim() else 0
     shape = (n, cache.n_kv_heads, cache.head_dim)
@@ -502,7 +509,6 @@ def kv_append(cache: PagedKV, q, k, v, cu_tokens, start_pos, rope_theta: float, 
 def paged_attention_workspace(cache: PagedKV, n_q_heads: int, max_len: int):
     """A workspace for paged_attention calls of these sizes (zero-filled uint8
     CUDA tensor; calls that may overlap on the device need one each)."""
-    import torch
     n = C.c_size_t()
     with torch.cuda.device(cache.dev):
         _check(_lib.mk_paged_attention_workspace(cache._ref, max_len, n_q_heads, C.byref(n)),
@@ -516,8 +522,12 @@ def paged_attention(cache: PagedKV, q, kv_lens, max_len: int, out, workspace=Non
     [n_seqs][n_q_heads][d]; kv_lens int32 [n_seqs], at most max_len (a host
     number); scale defaults to 1 / sqrt(d).  Without a workspace one is
     allocated for the call on its stream."""
-    import torch
-    what, dev, dt, i32, d = "paged_attention", cache.dev, cache.dtype, torch.int32, cache.head_dim
+    d = cache.head_dim
+    scale = d ** -0.5 if scale is None else scale
+    if stream is None and workspace is not None and not _fast.paged_attention(
+            cache._addr, cache.dev, q, kv_lens, max_len, out, workspace, scale, status):
+        return
+    what, dev, dt, i32 = "paged_attention", cache.dev, cache.dtype, torch.int32
     nq = q.shape[1] if q.dim() == 3 else 0
     shape = (cache.n_seqs, nq, d)
     qs = _rows(what, "q", q, dt, dev, shape)
@@ -529,15 +539,17 @@ def paged_attention(cache: PagedKV, q, kv_lens, max_len: int, out, workspace=Non
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         _invalid(what, "workspace must be contiguous on the cache's device")
     _launch(what, _lib.mk_paged_attention, dev, stream,
-            (cache._ref, lens, max_len, nq, q.data_ptr(), qs, d ** -0.5 if scale is None else scale, out.data_ptr(),
-             os_, workspace.data_ptr(), workspace.nbytes, _vec(what, "status", status, i32, dev, 1)))
+            (cache._ref, lens, max_len, nq, q.data_ptr(), qs, scale, out.data_ptr(), os_, workspace.data_ptr(), workspace.nbytes,
+             _vec(what, "status", status, i32, dev, 1)))
 
 
 def prompt_attention(q, k, v, cu_seqlens, max_len: int, out, scale=None, status=None, stream=None):
     """mk_prompt_attention: causal attention over packed prompts.  q, out
     [n][n_q_heads][d], k, v [n][n_kv_heads][d], cu_seqlens int32 [n_seqs + 1],
     max_len a host bound on the lengths; scale defaults to 1 / sqrt(d)."""
-    import torch
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    if stream is None and not _fast.prompt_attention(q, k, v, cu_seqlens, max_len, out, scale, status):
+        return
     what, dev, dt, i32 = "prompt_attention", q.get_device(), q.dtype, torch.int32
     code = _dtype_code(dt)
     if q.dim() != 3 or k.dim() != 3 or cu_seqlens.dim() != 1 or dev < 0 or code < 0:
@@ -554,15 +566,15 @@ def prompt_attention(q, k, v, cu_seqlens, max_len: int, out, scale=None, status=
         return
     _launch(what, _lib.mk_prompt_attention, dev, stream,
             (code, nq, nkv, d, cu, ns, n, max_len, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-             d ** -0.5 if scale is None else scale, out.data_ptr(), os_,
-             _vec(what, "status", status, i32, dev, 1)))
+             scale, out.data_ptr(), os_, _vec(what, "status", status, i32, dev, 1)))
 
 
 def sample(logits, uniform, token_out, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
     """mk_sample: one token per row of float32 logits [rows][vocab] (rows may
     be strided) from the given uniform numbers; the parameters are vectors of
     one value per row, or None (temperature 1, filter off)."""
-    import torch
+    if stream is None and not _fast.sample(logits, uniform, token_out, temperature, top_k, top_p, min_p):
+        return
     what, dev, f, i = "sample", logits.get_device(), torch.float32, torch.int32
     if logits.dim() != 2 or logits.dtype is not f or dev < 0:
         _invalid(what, "logits must be a float32 CUDA tensor [rows][vocab]")
