@@ -32,10 +32,10 @@ namespace mk {
 namespace {
 
 constexpr int kMaxBlocksPerSm = 2;
-// A block's part of an item is at least kMinSteps steps; an item costs a block
-// about kItemCost steps whatever its length (one 128-position item a block:
-// 5.4 us in all, 17 items of 2 steps after one another 30 us).
-constexpr int kMinSteps = 8, kItemCost = 16;
+// An item costs a block about this many steps whatever its length (one
+// 128-position item a block: 4.7 us in all, 17 items of 2 steps one after
+// another 30 us).
+constexpr int kItemCost = 16;
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t *p) {
     uint4 v;
@@ -72,6 +72,10 @@ template <int D>
 struct PagedShape {
     static constexpr int kGran = D == 64 ? 2 : 1;    // 16-key groups per step
     static constexpr int kStep = 16 * kGran;         // keys per step: 8 KB of K and V
+    // least part of an item (4096 positions of 8 KV heads, 4 / 8 / 16 / 24 / 32
+    // steps: 9.3, 9.3, 9.4, 10.5, 11.8 us for 64 dims, 12.6, 12.6, 10.2, 12.0,
+    // 12.7 for 128)
+    static constexpr int kMinSteps = D == 64 ? 8 : 16;
     static constexpr int kWarps = D == 64 ? 8 : 6;
     static constexpr int kThreads = kWarps * 32;
 };
@@ -126,12 +130,12 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
     const bool single = 2 * all_items <= P;
     int per, lo, hi;
     if (single) {
-        per = max((total + P - all_items - 1) / (P - all_items), kMinSteps);
+        per = max((total + P - all_items - 1) / (P - all_items), S::kMinSteps);
         lo = blk;
         hi = P;
     } else {
         total += all_items * kItemCost;
-        per = max((total - 1) / P + 1, kMinSteps);
+        per = max((total - 1) / P + 1, S::kMinSteps);
         lo = min(blk * per, total);   // blk * per < total + P * kMinSteps
         hi = min(total, lo + per);
     }
@@ -470,8 +474,9 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
 static int max_blocks(int num_sms) { return kMaxBlocksPerSm * num_sms; }
 
 static int grid_of(const mk_paged_kv &kv, int max_len, int num_sms) {
-    const int step = kv.head_dim == 64 ? PagedShape<64>::kStep : PagedShape<128>::kStep;
-    const long long want = (long long)kv.n_seqs * kv.n_kv_heads * ((max_len + step * kMinSteps - 1) / (step * kMinSteps));
+    const int least = kv.head_dim == 64 ? PagedShape<64>::kStep * PagedShape<64>::kMinSteps
+                                        : PagedShape<128>::kStep * PagedShape<128>::kMinSteps;
+    const long long want = (long long)kv.n_seqs * kv.n_kv_heads * ((max_len + least - 1) / least);
     return (int)(want < 1 ? 1 : want > max_blocks(num_sms) ? max_blocks(num_sms) : want);
 }
 

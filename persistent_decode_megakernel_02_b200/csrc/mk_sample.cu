@@ -23,6 +23,7 @@
 //
 // Rows beyond 8 blocks' shared memory take one block each that rereads them.
 #include <atomic>
+#include <utility>
 
 #include <cooperative_groups.h>
 
@@ -330,11 +331,15 @@ struct RegShared {
             uint32_t cnt[kBins];
         };
         uint32_t part[3][kBins];      // masses in three parts of 15, 14 and 14 bits
-        float maxima[kMaxCluster * kRegThreads];
+        u64 sums[kBins];              // and put together
+        struct {
+            float maxima[kMaxCluster * kRegThreads];
+            uint32_t bins[kBins];
+        };
     };
-    uint32_t bins[kBins];
     u64 list[kListMax];               // gathered logits: key, then lowest index first
     u64 sorted[kListMax];
+    ulonglong2 kept[kListMax];
     u64 sub[kRegWarps];
     double table[32];
     // written by every block of the cluster, read by all
@@ -342,7 +347,9 @@ struct RegShared {
     uint32_t x_cnt[kMaxCluster];
     u64 found_mass;
     uint32_t found_bin, found_before, found_cnt;
-    float top, bound, cut;
+    float warp_top[kMaxCluster * kRegWarps];
+    float top, cut;
+    int edge;
     int32_t last;
     uint32_t list_n;
     u64 tmp64[kRegWarps];
@@ -411,21 +418,45 @@ __device__ __forceinline__ u64 reg_block_scan(u64 v, u64 *tmp, u64 &total) {
     return before + x - v;
 }
 
-// A block's slice of the row is 16 warps' parts of IT vector steps (4 logits a
+// With more rows than fit the device at once, those with top-p alone, which
+// take about twice as long, come first: the row of cluster c in that order.
+__device__ __forceinline__ int row_in_order(const SampleArgs &a, int c) {
+    const int lane = threadIdx.x & 31;
+    auto slow = [&](int r) {
+        if (r >= a.rows || !(a.top_p[r] < 1.f)) return false;
+        const int k = a.top_k ? a.top_k[r] : 0;
+        return !(k > 0 && k < a.vocab);
+    };
+    for (int pass = 0; pass < 2; ++pass)
+        for (int r0 = 0; r0 < a.rows; r0 += 32) {
+            const bool mine = slow(r0 + lane) == (pass == 0) && r0 + lane < a.rows;
+            const unsigned m = __ballot_sync(0xffffffffu, mine);
+            if (c < __popc(m)) return r0 + __fns(m, 0, c + 1);
+            c -= __popc(m);
+        }
+    return 0;      // not reached: every row is one or the other
+}
+
+// A block's slice of the row is 16 warps\' parts of IT vector steps (4 logits a
 // lane), so index order is (warp, step, lane, element).  A thread only ever
 // reads the logits it stored; NaN is stored as -infinity.
-__global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, int IT) {
+__global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, int IT, bool in_order) {
     extern __shared__ float4 xs[];
     __shared__ __align__(16) RegShared sh;
     cg::cluster_group cl = cg::this_cluster();
     const int CL = cl.num_blocks(), rank = cl.block_rank();
-    const int row = blockIdx.x / CL, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.vocab;
+    const int row = in_order ? row_in_order(a, blockIdx.x / CL) : blockIdx.x / CL;
     const float *x = a.logits + (long long)row * a.stride;
-    const int V = a.vocab;
     RegShared *home = cl.map_shared_rank(&sh, 0);
 
+    auto started = cl.barrier_arrive();     // every block has, before the first write to another's memory
     fill_table(sh.table);
-    if (tid == 0) sh.list_n = 0;
+    if (tid == 0) {
+        sh.list_n = 0;
+        sh.edge = -1;
+    }
+    for (int i = tid; i < kBins; i += kRegThreads) sh.bins[i] = 0;
     const float t = a.temperature ? a.temperature[row] : 1.f;
     const int k = a.top_k ? a.top_k[row] : 0;
     const float p = a.top_p ? a.top_p[row] : 1.f;
@@ -476,6 +507,7 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
     };
     auto logit_of = [](u64 id) { return key_logit((uint32_t)(id >> 32)); };
 
+    cl.barrier_wait(std::move(started));
     Weight wt;
     const bool by_k = k > 0 && k < V, by_p = p < 1.f;
     float top;
@@ -483,23 +515,26 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
     if (by_k && k <= kMaxK && t > 0.f) {
         // ---- top-k by the threads' maxima
         home->maxima[rank * kRegThreads + tid] = best;
+        const float wm = warp_max(best);
+        if (lane < CL) cl.map_shared_rank(&sh, lane)->warp_top[rank * kRegWarps + warp] = wm;
         cl.sync();
+        top = -INFINITY;
+        for (int i = lane; i < CL * kRegWarps; i += 32) top = fmaxf(top, sh.warp_top[i]);
+        top = warp_max(top);
+        if (top == -INFINITY) {
+            if (rank == 0 && tid == 0) a.token[row] = -1;
+            return;
+        }
+        wt.init(a, row, top, t, sh.table);
+        const float scale = fminf(64.f / t, 1e30f);
+        auto bin_of = [&](float f) { return f == top ? 0 : (int)fminf((top - f) * scale, (float)(kBins - 1)); };
         if (rank == 0) {
-            float mk[kMaxCluster], m = -INFINITY;
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r) {
-                mk[r] = r < CL ? sh.maxima[r * kRegThreads + tid] : -INFINITY;
-                m = fmaxf(m, mk[r]);
-            }
-            m = block_max(m, reinterpret_cast<float *>(sh.tmp64));
-            for (int i = tid; i < kBins; i += kRegThreads) sh.bins[i] = 0;
-            if (tid == 0) sh.found_bin = 0xffffffffu;
-            __syncthreads();
-            const float scale = fminf(64.f / t, 1e30f);
-            auto bin_of = [&](float f) { return f == m ? 0 : (int)fminf((m - f) * scale, (float)(kBins - 1)); };
 #pragma unroll
             for (int r = 0; r < kMaxCluster; ++r)
-                if (mk[r] > -INFINITY) atomicAdd(&sh.bins[bin_of(mk[r])], 1u);
+                if (r < CL) {
+                    const float m = sh.maxima[r * kRegThreads + tid];
+                    if (m > -INFINITY) atomicAdd(&sh.bins[bin_of(m)], 1u);
+                }
             __syncthreads();
             const uint4 c = reinterpret_cast<const uint4 *>(sh.bins)[tid];
             uint32_t s = c.x + c.y + c.z + c.w, run = s;
@@ -518,53 +553,40 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
                 if (y < (uint32_t)k) { b = 1; y += c.y; }
                 if (y < (uint32_t)k) { b = 2; y += c.z; }
                 if (y < (uint32_t)k) b = 3;
-                sh.found_bin = 4 * tid + b;
-            }
-            __syncthreads();
-            // the smallest maximum of the bins up to it: at least k logits are no smaller
-            const uint32_t edge = sh.found_bin;
-            float low = INFINITY;
-            if (edge != 0xffffffffu)
-#pragma unroll
-                for (int r = 0; r < kMaxCluster; ++r)
-                    if (mk[r] > -INFINITY && bin_of(mk[r]) <= (int)edge) low = fminf(low, mk[r]);
-            low = -block_max(-low, reinterpret_cast<float *>(sh.tmp64));
-            if (tid < CL) {
-                RegShared *o = cl.map_shared_rank(&sh, tid);
-                o->top = m;
-                o->bound = edge != 0xffffffffu ? low : -INFINITY;
+                for (int r = 0; r < CL; ++r) cl.map_shared_rank(&sh, r)->edge = 4 * tid + b;
             }
         }
         cl.sync();
-        top = sh.top;
-        const float bound = sh.bound;
-        if (top == -INFINITY) {
-            if (rank == 0 && tid == 0) a.token[row] = -1;
-            return;
-        }
-        wt.init(a, row, top, t, sh.table);
-        if (bound > -INFINITY && top < INFINITY) {
+        // at least k logits lie in the bins up to it (not the last: all the rest)
+        const int edge = sh.edge;
+        if (edge >= 0 && edge < kBins - 1 && top < INFINITY) {
             each([&](float f, int i) {
-                if (f >= bound) gather(f, i);
+                if (bin_of(f) <= edge) gather(f, i);
             });
             cl.sync();
             const uint32_t n = home->list_n;
             if (n <= kListMax) {
                 if (rank != 0) return;
                 sort_descending(sh.list, sh.sorted, (int)n);
-                u64 id = tid < n ? sh.sorted[tid] : 0, total;
+                const u64 id = tid < n ? sh.sorted[tid] : 0;
+                u64 total;
                 u64 w = tid < n && tid < k ? wt.whole(logit_of(id)) : 0;
                 const u64 before = reg_block_scan(w, sh.tmp64, total);
                 if (by_p && tid > 0 && !((double)before < (double)p * (double)total)) w = 0;
                 if (wt.min_v > 0.0 && w > 0 && !wt.enough(logit_of(id))) w = 0;
-                // in index order, the dropped ones with weight 0
-                if (tid < n) sh.list[tid] = id << 32 | (w ? id >> 32 : 0);
-                __syncthreads();
-                sort_descending(sh.list, sh.sorted, (int)n);
-                id = tid < n ? sh.sorted[tid] : 0;
-                w = (uint32_t)id ? wt.whole(key_logit((uint32_t)id)) : 0;
-                const u64 run = reg_block_scan(w, sh.tmp64, total), goal = goal_of(a.uniform[row], total);
-                if (goal >= run && goal < run + w) a.token[row] = (int)~(uint32_t)(id >> 32);
+                // what lies ahead in index order: the list again, as (~index, weight)
+                if (tid < n) sh.kept[tid] = make_ulonglong2((uint32_t)id, w);
+                u64 run = 0;
+                const u64 kept = reg_block_sum(w, sh.tmp64);      // synchronises
+                if (w) {
+#pragma unroll 4
+                    for (uint32_t j = 0; j < n; ++j) {
+                        const ulonglong2 o = sh.kept[j];
+                        run += o.x > (uint32_t)id ? o.y : 0;
+                    }
+                    const u64 goal = goal_of(a.uniform[row], kept);
+                    if (goal >= run && goal < run + w) a.token[row] = (int)~(uint32_t)id;
+                }
                 cl.sync();      // the others have read the count (or are gone)
                 return;
             }
@@ -681,7 +703,7 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
         auto bin_of = [&](float f) { return f == top ? 0 : (int)fminf((top - f) * scale, (float)(kBins - 1)); };
         for (int i = tid; i < 3 * kBins; i += kRegThreads) sh.part[0][i] = 0;
         __syncthreads();
-        // a block's sum of 2^14 parts of 15 bits fits 32 bits.  The last bin
+        // a block's sum of 45056 parts of 15 bits fits 32 bits.  The last bin
         // (16 units and more below the top) may hold most of a row: summed in
         // registers
         u64 rest = 0;
@@ -697,46 +719,48 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
         });
         rest = reg_block_sum(rest, sh.tmp64);
         if (tid < CL) cl.map_shared_rank(&sh, tid)->x_sum[rank] = rest;
-        cl.sync();
-        // every block sums a share of the bins, consecutive ones per thread
-        const int share = kBins / CL, per = max(share / kRegThreads, 1), lo = rank * share;
-        u64 m[4] = {0, 0, 0, 0}, msum = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int b = tid * per + i;
-            if (i < per && b < share)
-#pragma unroll
-                for (int r = 0; r < kMaxCluster; ++r)
-                    if (r < CL) {
-                        const RegShared *o = cl.map_shared_rank(&sh, r);
-                        m[i] += (u64)o->part[0][lo + b] + ((u64)o->part[1][lo + b] << 15) +
-                                ((u64)o->part[2][lo + b] << 29);
-                    }
-            msum += m[i];
+        // the parts together, four consecutive bins a thread, then over the
+        // blocks: every block finds the bin by itself
+        u64 m[4], msum = 0;
+        {
+            const uint4 p0 = reinterpret_cast<const uint4 *>(sh.part[0])[tid], p1 = reinterpret_cast<const uint4 *>(sh.part[1])[tid],
+                        p2 = reinterpret_cast<const uint4 *>(sh.part[2])[tid];
+            m[0] = p0.x + ((u64)p1.x << 15) + ((u64)p2.x << 29);
+            m[1] = p0.y + ((u64)p1.y << 15) + ((u64)p2.y << 29);
+            m[2] = p0.z + ((u64)p1.z << 15) + ((u64)p2.z << 29);
+            m[3] = p0.w + ((u64)p1.w << 15) + ((u64)p2.w << 29);
         }
-        u64 block_mass;
-        u64 at = reg_block_scan(msum, sh.tmp64, block_mass);
-        if (tid < CL) cl.map_shared_rank(&sh, tid)->x_mass[rank] = block_mass;
+        __syncthreads();
+        reinterpret_cast<ulonglong2 *>(sh.sums)[2 * tid] = make_ulonglong2(m[0], m[1]);
+        reinterpret_cast<ulonglong2 *>(sh.sums)[2 * tid + 1] = make_ulonglong2(m[2], m[3]);
         if (tid == 0) sh.found_bin = 0xffffffffu;
         cl.sync();
-        u64 all = 0;
-        for (int r = 0; r < CL; ++r) {
-            if (r < rank) at += sh.x_mass[r];
-            all += sh.x_mass[r] + sh.x_sum[r];
-        }
+#pragma unroll
+        for (int r = 1; r < kMaxCluster; ++r)
+            if (r < CL) {
+                const ulonglong2 *o = reinterpret_cast<const ulonglong2 *>(cl.map_shared_rank(&sh, (rank + r) % CL)->sums);
+                const ulonglong2 o0 = o[2 * tid], o1 = o[2 * tid + 1];
+                m[0] += o0.x;
+                m[1] += o0.y;
+                m[2] += o1.x;
+                m[3] += o1.y;
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) msum += m[i];
+        u64 all;
+        u64 at = reg_block_scan(msum, sh.tmp64, all);
+        for (int r = 0; r < CL; ++r) all += sh.x_sum[r];
         const double target = (double)p * (double)all;
         auto reached = [&](u64 mass) { return mass > 0 && (double)mass >= target; };    // the top is in bin 0
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (i < per && tid * per + i < share && !reached(at) && reached(at + m[i]))
-                for (int r = 0; r < CL; ++r) {
-                    RegShared *o = cl.map_shared_rank(&sh, r);
-                    o->found_bin = lo + tid * per + i;
-                    o->found_mass = at;
-                }
+            if (!reached(at) && reached(at + m[i])) {
+                sh.found_bin = 4 * tid + i;
+                sh.found_mass = at;
+            }
             at += m[i];
         }
-        cl.sync();
+        __syncthreads();
         if (sh.found_bin != 0xffffffffu) {
             const int bin = (int)sh.found_bin;
             each([&](float f, int i) {
@@ -776,8 +800,8 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
                 last = sh.last;
                 done_p = true;
             }
-            cl.sync();
         }
+        cl.sync();      // the sums and the cut are read
     }
 
     // The index at which the running sum of weight(logit, index), in index
@@ -911,7 +935,7 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
 
 }  // namespace
 
-cudaError_t sample_launch(const SampleArgs &a, int device, int, cudaStream_t stream) {
+cudaError_t sample_launch(const SampleArgs &a, int device, int num_sms, cudaStream_t stream) {
     // Eight blocks a row from 8 vector steps each on; shorter rows take fewer.
     // (up to 3 logits ahead of a row that starts inside a 16-byte word)
     const int need = a.vocab + 3;
@@ -940,7 +964,7 @@ cudaError_t sample_launch(const SampleArgs &a, int device, int, cudaStream_t str
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sample_kernel, a, steps);
+    return cudaLaunchKernelEx(&cfg, sample_kernel, a, steps, a.top_p && (long long)a.rows * cluster > 2 * num_sms);
 }
 
 }  // namespace mk
