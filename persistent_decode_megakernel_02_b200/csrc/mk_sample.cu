@@ -560,9 +560,18 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
         // at least k logits lie in the bins up to it (not the last: all the rest)
         const int edge = sh.edge;
         if (edge >= 0 && edge < kBins - 1 && top < INFINITY) {
-            each([&](float f, int i) {
-                if (bin_of(f) <= edge) gather(f, i);
-            });
+            const float beyond = (float)(edge + 1);
+            auto in = [&](float f) { return (top - f) * scale < beyond; };      // bin_of(f) <= edge
+#pragma unroll 4
+            for (int it = 0; it < IT; ++it) {
+                const float4 q = xs[it * kRegThreads + tid];
+                const int i = base + it * 128;
+                if (!in(fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)))) continue;
+                if (in(q.x)) gather(q.x, i);
+                if (in(q.y)) gather(q.y, i + 1);
+                if (in(q.z)) gather(q.z, i + 2);
+                if (in(q.w)) gather(q.w, i + 3);
+            }
             cl.sync();
             const uint32_t n = home->list_n;
             if (n <= kListMax) {
