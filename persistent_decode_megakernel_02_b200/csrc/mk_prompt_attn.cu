@@ -162,6 +162,35 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
     }
     if (warp < 8)
         for (int i = tid; i < 2 * 3 * 128; i += 256) (&t.first[0][0][0])[i] = 0x7fffffff;
+    // the loader's view of the work, begun while the others set up: level l of
+    // a sequence is its row blocks R l .. R l + R - 1
+    const int G = a.nq / a.nkv, R = G & 1 ? 2 : 1;
+    const int per_seq = G * R / 2 * a.nkv;            // items of a sequence at a level
+    int row0 = 0, len = 0;      // of sequence s0 + lane
+    auto levels_of = [&](int s) {
+        row0 = len = 0;
+        if (s < a.n_seqs) {
+            const int b = a.cu[s], e = a.cu[s + 1];
+            if (b >= 0 && e >= b && e <= a.n_tokens && e - b <= a.max_len) {
+                row0 = b;
+                len = e - b;
+            }
+        }
+        return (len + kTile * R - 1) / (kTile * R);
+    };
+    auto count = [&](int level) {       // sequences that have it
+        int c = 0;
+        for (int s0 = 0; s0 < a.n_seqs; s0 += 32)
+            c += __popc(__ballot_sync(0xffffffffu, levels_of(s0 + lane) > level));
+        return c;
+    };
+    int level = 0, here = 0;
+    if (warp == 8) {
+        if (lane < 3) tma_prefetch_map(lane == 0 ? &p.q : lane == 1 ? &p.k : &p.v);
+        for (int s0 = 0; s0 < a.n_seqs; s0 += 32) level = max(level, levels_of(s0 + lane));
+        level = __reduce_max_sync(0xffffffffu, level) - 1;
+        here = level >= 0 ? count(level) : 0;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -170,30 +199,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
     if (warp >= 8) set_regs_down<kControlRegsPrompt>();
     if (warp == 8) {
         // ---- scheduler and loader
-        const int G = a.nq / a.nkv, R = G & 1 ? 2 : 1;    // row blocks of a level
-        const int per_seq = G * R / 2 * a.nkv;            // items of a sequence at a level
-        int row0 = 0, len = 0;      // of sequence s0 + lane
-        auto levels_of = [&](int s) {
-            row0 = len = 0;
-            if (s < a.n_seqs) {
-                const int b = a.cu[s], e = a.cu[s + 1];
-                if (b >= 0 && e >= b && e <= a.n_tokens && e - b <= a.max_len) {
-                    row0 = b;
-                    len = e - b;
-                }
-            }
-            return (len + kTile * R - 1) / (kTile * R);
-        };
-        auto count = [&](int level) {
-            int c = 0;
-            for (int s0 = 0; s0 < a.n_seqs; s0 += 32)
-                c += __popc(__ballot_sync(0xffffffffu, levels_of(s0 + lane) > level));
-            return c;
-        };
-        int level = 0;
-        for (int s0 = 0; s0 < a.n_seqs; s0 += 32) level = max(level, levels_of(s0 + lane));
-        level = __reduce_max_sync(0xffffffffu, level) - 1;
-        int here = level >= 0 ? count(level) : 0;         // sequences with this level
         long long base = 0;                               // items before it
         const int P = gridDim.x;
         int k = 0, F = 0;     // items published, tiles loaded
