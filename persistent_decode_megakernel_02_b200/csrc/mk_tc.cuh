@@ -82,27 +82,22 @@ __device__ __forceinline__ void fence_mbar_init() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
-// Wait for a barrier's phase, bounded: after `kWaitNs` (or once another role
-// of the block has given up) it returns false with *abort set.
-constexpr unsigned long long kWaitNs = 2000000000ull;
-__device__ __forceinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    const unsigned long long t0 = globaltimer();
-    while (true) {
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
-        if (globaltimer() - t0 > kWaitNs) {
+// Wait for a barrier's phase, bounded: after kWaitTries tries, each of which
+// may itself wait a while (seconds in all), or once another role of the block
+// has given up, it returns false with *abort set.  Kept to a few instructions:
+// it is inlined at every wait.
+constexpr uint32_t kWaitTries = 1u << 23;
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    uint32_t tries = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if ((++tries & 255u) == 0 && (tries >= kWaitTries || *abort)) {
             *abort = 1;
             return false;
         }
     }
+    return true;
 }
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    for (int i = 0; i < 16; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait_slow(bar, parity, abort);
-}
-
 // the same for a whole warp, with one answer
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
