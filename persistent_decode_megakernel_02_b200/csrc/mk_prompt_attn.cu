@@ -35,7 +35,6 @@
 #include <cuda.h>
 
 #include <atomic>
-#include <type_traits>
 
 #include "mk_tc.cuh"
 
@@ -50,33 +49,13 @@ constexpr int kPromptThreads = 384;
 // registers would not end: prompt_launch refuses any other launch count.
 constexpr int kLaunchRegsPrompt = 168, kSoftmaxRegs = 208, kControlRegsPrompt = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kControlRegsPrompt == kPromptThreads * kLaunchRegsPrompt, "register split");
-// One quarter of the pairs' first halves go to ex2_fma (of the exponentials:
-// one eighth); 0, 1/4, 1/2, 3/4 of them: 489, 479, 480, 485 us at 8192 tokens.
-constexpr int kPolyNum = 1, kPolyOf = 4;
 constexpr float kRescale = 8.f;            // exponent headroom before O is rescaled
 
-// The larger of three, NaN if one is NaN.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+// The larger of three (NaN is left out, as by fmaxf).
+__device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
-}
-// 2^x of a pair by multiplications and additions, for x <= 127 (results below
-// 2^-126 are given as 2^-126; not for NaN): the nearest integer by adding
-// 1.5 * 2^23, and for the rest in [-1/2, 1/2] the cubic of least relative error
-// (7.5e-5, below the rounding of the weights to 16 bits).
-__device__ __forceinline__ float2 ex2_fma(float2 x) {
-    x.x = fmaxf(x.x, -126.f);
-    x.y = fmaxf(x.y, -126.f);
-    auto two = [](float v) { return make_float2(v, v); };
-    const float2 n = fadd2(x, two(12582912.f));
-    const float2 f = fadd2(n, two(-12582912.f));
-    const float2 r = ffma2(f, two(-1.f), x);
-    float2 p = ffma2(r, two(0.0551716685295105f), two(0.2426111251115799f));
-    p = ffma2(r, p, two(0.6932609677314758f));
-    p = ffma2(r, p, two(0.9999280571937561f));
-    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(n.x) << 23)),
-                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(n.y) << 23)));
 }
 
 template <int D>
@@ -125,6 +104,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
     PromptTail &t = *reinterpret_cast<PromptTail *>(smem + L::kTail);
     const PromptArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (smem_addr(smem) & 1023u) {      // the swizzled tiles need it; no static shared memory comes before
+        if (tid == 0) bad_value(a.status);
+        return;
+    }
 
     if (blockIdx.x == 0)
         for (int i = tid; i < a.n_seqs; i += kPromptThreads) {
@@ -396,39 +379,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                 asm volatile("bar.sync 1, 64;" ::: "memory");
             }
             for (int which = 0; which < J - blk0 && ok; ++which) {
-            // the issuer says when the tile is there: a wait on the tile's own
-            // barrier from here could miss phases of the tiles before it
-            const int j = blk0 + which, f = F + 2 * j + 1;
-            ok = mbar_wait_warp(&t.guard_go[which], masked[which]++ & 1, &t.abort) &&
-                 mbar_wait_warp(&t.full[f % L::kStages], (f / L::kStages) & 1, &t.abort);
-            if (!ok) break;
-            uint4 *tile = reinterpret_cast<uint4 *>(smem + L::kRing + f % L::kStages * L::kTileBytes);
-            constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u, kOne = kBf16 ? 0x00800080u : 0x04000400u;
-            uint32_t bad = 0;
+                // the issuer says when the tile is there: a wait on the tile's own
+                // barrier from here could miss phases of the tiles before it
+                const int j = blk0 + which, f = F + 2 * j + 1;
+                ok = mbar_wait_warp(&t.guard_go[which], masked[which]++ & 1, &t.abort) &&
+                     mbar_wait_warp(&t.full[f % L::kStages], (f / L::kStages) & 1, &t.abort);
+                if (!ok) break;
+                uint4 *tile = reinterpret_cast<uint4 *>(smem + L::kRing + f % L::kStages * L::kTileBytes);
+                constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u, kOne = kBf16 ? 0x00800080u : 0x04000400u;
+                uint32_t bad = 0;
 #pragma unroll 8
-            for (int i = gt; i < L::kTileBytes / 16; i += 64) {
-                const uint4 x = tile[i];
-                bad |= ((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne);
-            }
-            if (bad & 0x80008000u) {
-                uint16_t *e = reinterpret_cast<uint16_t *>(tile);
-                for (int i = gt; i < L::kTileBytes / 16; i += 64)
-                    for (int c = 0; c < 8; ++c) {
-                        const uint32_t w = e[i * 8 + c];
-                        if ((w & kExp & 0xffffu) != (kExp & 0xffffu)) continue;
-                        e[i * 8 + c] = 0;
-                        const int half = i / (kTile * 8), r = i / 8 % kTile;
-                        const int col = half * 64 + ((i ^ r) & 7) * 8 + c;
-                        if (j * kTile + r < len) {
-                            const int kind = (w & ~kExp & 0x7fffu) ? 0 : w & 0x8000u ? 2 : 1;
-                            atomicMin(&t.first[slot][kind][col], j * kTile + r);
-                            t.any[slot] = 1;
+                for (int i = gt; i < L::kTileBytes / 16; i += 64) {
+                    const uint4 x = tile[i];
+                    bad |= ((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne);
+                }
+                if (bad & 0x80008000u) {
+                    uint16_t *e = reinterpret_cast<uint16_t *>(tile);
+                    for (int i = gt; i < L::kTileBytes / 16; i += 64)
+                        for (int c = 0; c < 8; ++c) {
+                            const uint32_t w = e[i * 8 + c];
+                            if ((w & kExp & 0xffffu) != (kExp & 0xffffu)) continue;
+                            e[i * 8 + c] = 0;
+                            const int half = i / (kTile * 8), r = i / 8 % kTile;
+                            const int col = half * 64 + ((i ^ r) & 7) * 8 + c;
+                            if (j * kTile + r < len) {
+                                const int kind = (w & ~kExp & 0x7fffu) ? 0 : w & 0x8000u ? 2 : 1;
+                                atomicMin(&t.first[slot][kind][col], j * kTile + r);
+                                t.any[slot] = 1;
+                            }
                         }
-                    }
-                fence_async_smem();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&t.guard_done[which]);
+                    fence_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&t.guard_done[which]);
             }
             if (lane == 0) mbar_arrive(&t.item_empty[slot]);
             F += 2 * J;
@@ -445,71 +428,73 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
         int tiles = 0, outs = 0, pvs = 0;      // phases so far
         bool ok = true;
         for (int k = 0; ok; ++k) {
-        const int slot = k & 1;
-        ok = mbar_wait_warp(&t.item_full[slot], (k >> 1) & 1, &t.abort);
-        if (!ok || t.item[slot].tiles == 0) break;
-        const int n = t.item[slot].n[u], blk = t.item[slot].blk[u];
-        float m = -INFINITY, l = 0.f;
-        for (int j = 0; j < n && ok; ++j) {
-            // S of this tile (for 128 dims the products of the tile before are
-            // done too: one thread issues all of them, in this order)
-            ok = mbar_wait_warp(&t.s_full[u], tiles++ & 1, &t.abort);
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t x[4][32];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, x[q]);
-            tmem_ld_wait();
-            if constexpr (kOwnP) {      // S is read: the next tile's may be computed
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&t.s_free[u]);
-            }
-            if (j == blk)      // the diagonal: keys beyond the row's own are not seen
-#pragma unroll
-                for (int i = 0; i < kTile; ++i)
-                    if (i > r) x[i / 32][i % 32] = 0xff800000u;
-            auto at = [&](int i) { return __uint_as_float(x[i / 32][i % 32]); };
-            float top4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top4[i] = max3_nan(at(i), at(i + 4), at(i + 8));
-#pragma unroll
-            for (int i = 12; i < kTile - 4; i += 8)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) top4[k] = max3_nan(top4[k], at(i + k), at(i + k + 4));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) top4[k] = max3_nan(top4[k], at(kTile - 4 + k), top4[k]);
-            const float top = max3_nan(max3_nan(top4[0], top4[1], top4[2]), top4[3], top4[3]);
-            const float old = m;
-            if (!((top - m) * c <= kRescale)) m = fmaxf(m, top);
-            const bool raise = m != old;
-            // P and O are free once the tile before is weighted (128 dims: it is)
-            auto weighted = [&] {
-                if (!kOwnP || j == 0) return true;
-                const bool done = mbar_wait_warp(&t.pv_done[u], pvs & 1, &t.abort);
-                tc_fence_after();
-                return done;
-            };
-            if (__any_sync(0xffffffffu, raise)) {
-                const float f = raise ? ex2((old - m) * c) : 1.f;
-                l *= f;
-                ok = weighted();
+            const int slot = k & 1;
+            ok = mbar_wait_warp(&t.item_full[slot], (k >> 1) & 1, &t.abort);
+            if (!ok || t.item[slot].tiles == 0) break;
+            const int n = t.item[slot].n[u], blk = t.item[slot].blk[u];
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < n && ok; ++j) {
+                // S of this tile (for 128 dims the products of the tile before are
+                // done too: one thread issues all of them, in this order)
+                ok = mbar_wait_warp(&t.s_full[u], tiles++ & 1, &t.abort);
                 if (!ok) break;
-                if (j > 0)
-#pragma unroll 1
-                    for (int q = 0; q < D / 16; ++q) {
-                        uint32_t o[16];
-                        tmem_ld16(to + q * 16, o);
-                        tmem_ld_wait();
+                tc_fence_after();
+                uint32_t x[4][32];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st16(to + q * 16, o);
-                    }
-            }
-            const float mc = m == -INFINITY ? 0.f : m * c;
-            const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
-            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-            auto weights = [&](auto mixed) {
+                for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, x[q]);
+                tmem_ld_wait();
+                if constexpr (kOwnP) {      // S is read: the next tile's may be computed
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&t.s_free[u]);
+                }
+                if (j == blk)      // the diagonal: keys beyond the row's own are not seen
+#pragma unroll
+                    for (int i = 0; i < kTile; ++i)
+                        if (i > r) x[i / 32][i % 32] = 0xff800000u;
+                auto at = [&](int i) { return __uint_as_float(x[i / 32][i % 32]); };
+                float top4[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top4[i] = max3(at(i), at(i + 4), at(i + 8));
+#pragma unroll
+                for (int i = 12; i < kTile - 4; i += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top4[k] = max3(top4[k], at(i + k), at(i + k + 4));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top4[k] = max3(top4[k], at(kTile - 4 + k), top4[k]);
+                const float top = max3(max3(top4[0], top4[1], top4[2]), top4[3], top4[3]);
+                const float old = m;
+                if (!((top - m) * c <= kRescale)) m = fmaxf(m, top);
+                const bool raise = m != old;
+                // P and O are free once the tile before is weighted (128 dims: it is)
+                auto weighted = [&] {
+                    if (!kOwnP || j == 0) return true;
+                    const bool done = mbar_wait_warp(&t.pv_done[u], pvs & 1, &t.abort);
+                    tc_fence_after();
+                    return done;
+                };
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float f = raise ? ex2((old - m) * c) : 1.f;
+                    l *= f;
+                    ok = weighted();
+                    if (!ok) break;
+                    if (j > 0)
+#pragma unroll 1
+                        for (int q = 0; q < D / 16; ++q) {
+                            uint32_t o[16];
+                            tmem_ld16(to + q * 16, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st16(to + q * 16, o);
+                        }
+                }
+                const float mc = m == -INFINITY ? 0.f : m * c;
+                const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+                float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                // (a share of the exponentials on the FMA units, by a polynomial,
+                // changed nothing between none and a quarter: 460, 459, 462 us at
+                // 8192 tokens)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t w[16];
@@ -517,12 +502,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                     for (int i = 0; i < 32; i += 4) {
                         float2 e0 = ffma2(make_float2(at(q * 32 + i), at(q * 32 + i + 1)), c2, mc2);
                         float2 e1 = ffma2(make_float2(at(q * 32 + i + 2), at(q * 32 + i + 3)), c2, mc2);
-                        if (mixed.value && (i / 4) % kPolyOf < kPolyNum) {
-                            e0 = ex2_fma(e0);
-                        } else {
-                            e0.x = ex2(e0.x);
-                            e0.y = ex2(e0.y);
-                        }
+                        e0.x = ex2(e0.x);
+                        e0.y = ex2(e0.y);
                         e1.x = ex2(e1.x);
                         e1.y = ex2(e1.y);
                         sum0 = fadd2(sum0, e0);
@@ -533,75 +514,70 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                     if (q == 0) ok = weighted();
                     tmem_st16(tp + q * 16, w);      // (128 dims: over what this row has read of S)
                 }
-            };
-            // masked scores have to give exactly zero: the function unit alone
-            if (j == blk) weights(std::false_type());
-            else weights(std::true_type());
-            if (!ok) break;
-            if (kOwnP && j > 0) ++pvs;
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&t.p_ready[u]);
-            l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-            if (top != top) l = NAN;      // a score that is not a number
-        }
-        if (kOwnP && ok && n > 0) ok = mbar_wait_warp(&t.pv_done[u], pvs++ & 1, &t.abort);
-        if (ok && n > 0) ok = mbar_wait_warp(&t.o_full[u], outs++ & 1, &t.abort);
-        if (ok && n > 0) {
-            tc_fence_after();
-            const int pos = blk * kTile + r, len = t.item[slot].len;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            // rows leave through shared memory, eight rows of 64 bytes a store:
-            // one row a thread took 32 transactions a store instruction (the
-            // epilogue 7400 cycles at 128 dims)
-            uint4 *stage = reinterpret_cast<uint4 *>(smem + L::kStore + warp * 2048);
-            auto staged = [&](int row, int chunk) { return stage + row * 4 + (chunk ^ (row >> 1 & 3)); };
-            const int row_first = blk * kTile + (warp & 3) * 32;
-            uint16_t *dst = (uint16_t *)a.out + (long long)(t.item[slot].row0 + row_first) * a.out_stride +
-                            (long long)t.item[slot].head[u] * D;
-            const bool any = t.any[slot] != 0;
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-                uint32_t x[32];
-                tmem_ld32(to + q * 32, x);
-                tmem_ld_wait();
-                if (q == D / 32 - 1) {      // O is read: the next item may start its own
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&t.o_empty[u]);
-                }
-                if (any)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int col = q * 32 + i;
-                        float o = __uint_as_float(x[i]);
-                        if (t.first[slot][0][col] <= pos) o = NAN;
-                        if (t.first[slot][1][col] <= pos) o += INFINITY;
-                        if (t.first[slot][2][col] <= pos) o -= INFINITY;
-                        x[i] = __float_as_uint(o);
-                    }
-#pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    uint4 w;
-                    w.x = T::pack(__uint_as_float(x[i]) * inv, __uint_as_float(x[i + 1]) * inv);
-                    w.y = T::pack(__uint_as_float(x[i + 2]) * inv, __uint_as_float(x[i + 3]) * inv);
-                    w.z = T::pack(__uint_as_float(x[i + 4]) * inv, __uint_as_float(x[i + 5]) * inv);
-                    w.w = T::pack(__uint_as_float(x[i + 6]) * inv, __uint_as_float(x[i + 7]) * inv);
-                    *staged(lane, i / 8) = w;
-                }
+                if (!ok) break;
+                if (kOwnP && j > 0) ++pvs;
+                tmem_st_wait();
+                tc_fence_before();
                 __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = i * 8 + (lane >> 2), chunk = lane & 3;
-                    if (row_first + row < len)
-                        *reinterpret_cast<uint4 *>(dst + row * a.out_stride + q * 32 + chunk * 8) = *staged(row, chunk);
-                }
-                __syncwarp();
+                if (lane == 0) mbar_arrive(&t.p_ready[u]);
+                l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
             }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&t.item_empty[slot]);
+            if (kOwnP && ok && n > 0) ok = mbar_wait_warp(&t.pv_done[u], pvs++ & 1, &t.abort);
+            if (ok && n > 0) ok = mbar_wait_warp(&t.o_full[u], outs++ & 1, &t.abort);
+            if (ok && n > 0) {
+                tc_fence_after();
+                const int pos = blk * kTile + r, len = t.item[slot].len;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                // rows leave through shared memory, eight rows of 64 bytes a store:
+                // one row a thread took 32 transactions a store instruction (the
+                // epilogue 7400 cycles at 128 dims)
+                uint4 *stage = reinterpret_cast<uint4 *>(smem + L::kStore + warp * 2048);
+                auto staged = [&](int row, int chunk) { return stage + row * 4 + (chunk ^ (row >> 1 & 3)); };
+                const int row_first = blk * kTile + (warp & 3) * 32;
+                uint16_t *dst = (uint16_t *)a.out + (long long)(t.item[slot].row0 + row_first) * a.out_stride +
+                                (long long)t.item[slot].head[u] * D;
+                const bool any = t.any[slot] != 0;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t x[32];
+                    tmem_ld32(to + q * 32, x);
+                    tmem_ld_wait();
+                    if (q == D / 32 - 1) {      // O is read: the next item may start its own
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&t.o_empty[u]);
+                    }
+                    if (any)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int col = q * 32 + i;
+                            float o = __uint_as_float(x[i]);
+                            if (t.first[slot][0][col] <= pos) o = NAN;
+                            if (t.first[slot][1][col] <= pos) o += INFINITY;
+                            if (t.first[slot][2][col] <= pos) o -= INFINITY;
+                            x[i] = __float_as_uint(o);
+                        }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint4 w;
+                        w.x = T::pack(__uint_as_float(x[i]) * inv, __uint_as_float(x[i + 1]) * inv);
+                        w.y = T::pack(__uint_as_float(x[i + 2]) * inv, __uint_as_float(x[i + 3]) * inv);
+                        w.z = T::pack(__uint_as_float(x[i + 4]) * inv, __uint_as_float(x[i + 5]) * inv);
+                        w.w = T::pack(__uint_as_float(x[i + 6]) * inv, __uint_as_float(x[i + 7]) * inv);
+                        *staged(lane, i / 8) = w;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = i * 8 + (lane >> 2), chunk = lane & 3;
+                        if (row_first + row < len)
+                            *reinterpret_cast<uint4 *>(dst + row * a.out_stride + q * 32 + chunk * 8) = *staged(row, chunk);
+                    }
+                    __syncwarp();
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&t.item_empty[slot]);
         }
     }
 
