@@ -450,8 +450,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                 }
                 if (j == blk)      // the diagonal: keys beyond the row's own are not seen
 #pragma unroll
-                    for (int i = 0; i < kTile; ++i)
-                        if (i > r) x[i / 32][i % 32] = 0xff800000u;
+                    for (int q = 0; q < 4; ++q) {
+                        const int n = r + 1 - q * 32;      // of these 32 are seen
+                        const uint32_t hide = n <= 0 ? 0xffffffffu : n >= 32 ? 0u : 0xffffffffu << n;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (hide >> i & 1u) x[q][i] = 0xff800000u;
+                    }
                 auto at = [&](int i) { return __uint_as_float(x[i / 32][i % 32]); };
                 float top4[4];
 #pragma unroll
