@@ -512,8 +512,10 @@ int mk_decode_step_static(const mk_config *cfg, const mk_packed_weights *w, cons
  *    least the row they hold; anything else is MK_ERR_INVALID.
  *  - status_out: device int32 [1] or NULL.  A call that meets a bad value in
  *    device memory (see each operator) writes MK_ERR_INVALID there in
- *    stream order and works on without it; the word is never cleared by
- *    these calls, so the caller zeroes it once and looks when it likes.
+ *    stream order and works on without it (MK_ERR_TIMEOUT: a wait inside
+ *    mk_prompt_attention ran out, its outputs are not defined); the word is
+ *    never cleared by these calls, so the caller zeroes it once and looks
+ *    when it likes.
  *  - A device other than compute capability 10.0 gives MK_ERR_INVALID, a
  *    failed launch MK_ERR_CUDA.
  */
@@ -559,8 +561,8 @@ typedef struct mk_paged_kv {
  *              0, 1, 2, ...
  *   start_pos  device int32 [n_seqs]: position of the sequence's first new
  *              token; the others follow.
- *   n_tokens   rows of q, k and v; rows from cu_tokens[n_seqs] on are neither
- *              read nor written.
+ *   n_tokens   rows of q, k and v; rows from cu_tokens[n_seqs] on are left as
+ *              they were.
  *   q, q_out   [n_tokens][n_q_heads][head_dim]; both NULL (n_q_heads = 0):
  *              only k is rotated.  q_out may be q.
  *   k, v       [n_tokens][n_kv_heads][head_dim].
@@ -643,9 +645,9 @@ int mk_prompt_attention(int dtype, int n_q_heads, int n_kv_heads, int head_dim, 
  *      running sum of w exceeds uniform * (sum over all kept).
  * Weights are computed in 64 bits and summed as 64-bit integers (in units of
  * 2^-43 of the largest), so the result does not depend on any order of
- * summation; weights below that unit count as zero.
+ * summation; weights below half that unit count as zero.
  *   logits       device float [rows][vocab], row_stride (>= vocab) elements
- *                between rows; vocab <= MK_MAX_VOCAB
+ *                between rows; vocab <= MK_MAX_VOCAB, rows <= 2^24
  *   uniform      device float [rows], in [0, 1) (values outside are clamped)
  *   temperature  device float [rows]; not above 0: the row's argmax (lowest
  *                index), the filters and uniform unused.  NULL: 1.

@@ -85,7 +85,7 @@ def test_paged_refusals(bad):
 
 @pytest.mark.parametrize("bad", [
     dict(dtype=2), dict(nq=5), dict(nq=0), dict(nkv=0), dict(nq=18), dict(d=80), dict(d=256), dict(cu=None),
-    dict(cu=A + 2), dict(ns=0), dict(n=-1), dict(max_len=-1), dict(q=None), dict(qs=255), dict(qs=0), dict(k=A + 2),
+    dict(cu=A + 2), dict(ns=0), dict(n=-1), dict(n=(1 << 31) - 1), dict(max_len=-1), dict(q=None), dict(qs=255), dict(qs=0), dict(k=A + 2),
     dict(ks=64), dict(v=None), dict(vs=129), dict(scale=0.0), dict(scale=math.nan), dict(out=None), dict(os=192),
     dict(status=A + 3)], ids=str)
 def test_prompt_refusals(bad):
@@ -93,7 +93,7 @@ def test_prompt_refusals(bad):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(logits=None), dict(logits=A + 2), dict(stride=99), dict(rows=-1), dict(vocab=0), dict(u=None),
+    dict(logits=None), dict(logits=A + 2), dict(stride=99), dict(rows=-1), dict(rows=(1 << 24) + 1), dict(vocab=0), dict(u=None),
     dict(vocab=mk.MAX_VOCAB + 1, stride=1 << 21), dict(out=None), dict(out=A + 1), dict(t=A + 2), dict(k=A + 1),
     dict(p=A + 3), dict(m=A + 2)], ids=str)
 def test_sample_refusals(bad):
@@ -103,11 +103,17 @@ def test_sample_refusals(bad):
 def test_workspace_refusals():
     n = C.c_size_t(7)
     ask = lambda c, m, nq: lib.mk_paged_attention_workspace(C.byref(c), m, nq, C.byref(n))
-    for c, m, nq in ((cache(head_dim=32), 10, 4), (cache(), 65, 4), (cache(), -1, 4), (cache(), 10, 5),
+    for c, m, nq in ((cache(head_dim=32), 10, 4), (cache(num_pages=1 << 30), 10, 4), (cache(), 65, 4), (cache(), -1, 4), (cache(), 10, 5),
                      (cache(), 10, 0)):
         assert ask(c, m, nq) == mk.MK_ERR_INVALID and n.value == 0
     assert lib.mk_paged_attention_workspace(None, 1, 1, C.byref(n)) == mk.MK_ERR_INVALID
     assert lib.mk_paged_attention_workspace(C.byref(cache()), 1, 4, None) == mk.MK_ERR_INVALID
+
+
+def test_paged_work_that_does_not_fit_an_int():
+    # shared pages can make a batch longer than any device's memory
+    c = cache(n_seqs=1 << 20, pages_per_seq=1 << 16, n_kv_heads=8)
+    assert paged(c, nq=8, q=A, qs=512, os=512, max_len=1 << 20) == mk.MK_ERR_INVALID
 
 
 def test_nothing_to_do_touches_no_device():

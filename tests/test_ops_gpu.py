@@ -711,6 +711,214 @@ def test_sample_in_a_graph_and_on_streams(mk):
     assert all(torch.equal(o, outs[0]) for o in outs)
 
 
+@pytest.mark.parametrize("vocab", [2045, 2048, 2049, 4093, 16384, 16387, 65536, 131069, 131070, 151936, 262144, 360448, 360446, 360449])
+def test_sample_vocabularies_at_the_slices_edges(mk, vocab):
+    sample_case(mk, noise(4, vocab, vocab), k=[0, 60, 0, 5], p=[1.0, 0.9, 0.9, 1.0], m=[0.0, 0.0, 0.0, 0.02])
+
+
+def test_sample_large_k_and_flat_rows(mk):
+    # beyond the candidates one block ranks: the exact cuts
+    x = noise(6, 60000, 11, scale=0.02)
+    sample_case(mk, x, k=[385, 5000, 59999, 400, 0, 384], p=[1.0, 0.5, 0.9, 0.99, 0.7, 1.0], t=[1.0, 2.0, 0.5, 1.0, 3e3, 1.0])
+    x = noise(6, 60000, 12, scale=0.02, ties=True)
+    sample_case(mk, x, k=[385, 5000, 59999, 400, 0, 384], p=[1.0, 0.5, 0.9, 0.99, 0.7, 1.0])
+
+
+def test_sample_one_logit_far_above(mk):
+    x = noise(5, 50000, 13)
+    x[:, 49999] = 500.0
+    sample_case(mk, x, k=[1, 50, 0, 0, 0], p=[1.0, 0.9, 0.9, 1.0, 1.0], m=[0.0, 0.0, 0.0, 0.5, 0.0])
+    x[:, 7] = 500.0
+    sample_case(mk, x, k=[1, 50, 0, 0, 0], p=[1.0, 0.9, 0.4, 1.0, 1.0], m=[0.0, 0.0, 0.0, 1.0, 0.0])
+
+
+def test_sample_many_rows(mk):
+    rng = np.random.default_rng(0)
+    rows = 700
+    k = [int(v) for v in rng.choice([0, 0, 5, 40], rows)]
+    p = [float(v) for v in rng.choice([1.0, 0.6, 0.9], rows)]
+    sample_case(mk, noise(rows, 3001, 14), k=k, p=p)
+
+
+# ---- workspaces, shared pages, streams, both ways of the binding ------------------------
+
+def test_one_workspace_for_calls_of_other_sizes(mk):
+    g = gen(20)
+    big = make_cache(mk, g, [9000, 10, 700], 2, 128, 16, torch.bfloat16)
+    ws = mk.paged_attention_workspace(big, 8, 9000)
+    for lens, nq, nkv, d in (([9000, 10, 700], 8, 2, 128), ([33], 4, 1, 64), ([5000, 5000], 16, 2, 64), ([9000, 10, 700], 8, 2, 128)):
+        cache = big if len(lens) == 3 else make_cache(mk, g, lens, nkv, d, 16, torch.bfloat16)
+        need = mk.paged_attention_workspace(cache, nq, max(lens))
+        if need.numel() > ws.numel():
+            ws = need
+        q = torch.randn(len(lens), nq, d, generator=g, device="cuda").bfloat16()
+        out = torch.empty_like(q)
+        mk.paged_attention(cache, q, ints(lens), max(lens), out, ws)
+        paged_check(cache, q, lens, out, d ** -0.5)
+    torch.cuda.synchronize()
+    assert int(ws[:1024].max()) == 0          # the counters are ready for the next call
+
+
+def test_paged_sequences_that_share_pages(mk):
+    # a common prefix of three pages, read by four sequences
+    g = gen(21)
+    cache = make_cache(mk, g, [48, 60, 70, 90], 2, 64, 16, torch.float16)
+    cache.page_table[1:, :3] = cache.page_table[0, :3]
+    q = torch.randn(4, 4, 64, generator=g, device="cuda").half()
+    out = torch.empty_like(q)
+    lens = [48, 60, 70, 90]
+    mk.paged_attention(cache, q, ints(lens), 90, out)
+    paged_check(cache, q, lens, out, 0.125)
+
+
+@pytest.mark.parametrize("lens,max_len", [([0, 0, 0], 0), ([0] * 70, 16), ([1], 1)])
+def test_paged_nothing_or_next_to_nothing(mk, lens, max_len):
+    paged_case(mk, lens, 4, 2, 64, 16, torch.bfloat16, max_len=max_len)
+
+
+def test_paged_max_len_beyond_the_table(mk):
+    # one page of 16 a sequence: 50 tokens cannot be there
+    with pytest.raises(mk.MkError) as e:
+        paged_case(mk, [0] * 70, 4, 2, 64, 16, torch.bfloat16, max_len=50)
+    assert e.value.status == mk.MK_ERR_INVALID
+
+
+def test_prompt_many_sequences(mk):
+    rng = np.random.default_rng(1)
+    lens = [int(x) for x in rng.integers(0, 300, 200)]
+    prompt_case(mk, lens, 4, 1, 64, torch.bfloat16, seed=1)
+    prompt_case(mk, lens[:70], 3, 1, 128, torch.float16, seed=2)
+
+
+def test_calls_at_once_on_two_streams(mk):
+    # everything twice, on two streams at the same time, each with its own buffers
+    g = gen(22)
+    runs = []
+    for i, st in enumerate([torch.cuda.Stream(), torch.cuda.Stream()]):
+        lens = [1500 + 100 * i, 37, 0, 260]
+        n, cu = sum(lens), cu_of(lens)
+        cache = make_cache(mk, g, [m + 8 for m in lens], 2, 64, 16, torch.bfloat16)
+        q, k, v = (torch.randn(n, h, 64, generator=g, device="cuda").bfloat16() for h in (8, 2, 2))
+        x = noise(16, 32000, 30 + i)
+        runs.append(dict(st=st, lens=lens, cu=ints(cu), start=ints([0] * 4), cache=cache, q=q, k=k, v=v, out=torch.empty_like(q),
+                         q1=torch.randn(4, 8, 64, generator=g, device="cuda").bfloat16(), x=x, u=torch.rand(16, device="cuda"),
+                         token=torch.zeros(16, dtype=torch.int32, device="cuda"), kk=ints([40] * 16), l=ints(lens),
+                         ws=mk.paged_attention_workspace(cache, 8, 1500 + 100 * i)))
+        with pytest.raises(mk.MkError):               # beyond the table
+            mk.paged_attention_workspace(cache, 8, 1700)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for r in runs:
+            with torch.cuda.stream(r["st"]):
+                r["qr"], r["kr"], r["o1"] = torch.empty_like(r["q"]), torch.empty_like(r["k"]), torch.empty_like(r["q1"])
+                mk.kv_append(r["cache"], r["q"], r["k"], r["v"], r["cu"], r["start"], 1e4, r["qr"], r["kr"])
+                mk.prompt_attention(r["qr"], r["kr"], r["v"], r["cu"], 1700, r["out"])
+                mk.paged_attention(r["cache"], r["q1"], r["l"], max(r["lens"]), r["o1"], r["ws"])
+                mk.sample(r["x"], r["u"], r["token"], top_k=r["kk"])
+    torch.cuda.synchronize()
+    for r in runs:
+        prompt_check(r["qr"], r["kr"], r["v"], r["lens"], r["out"], 0.125)
+        paged_check(r["cache"], r["q1"], r["lens"], r["o1"], 0.125)
+        want = [sample_reference(a, 1.0, 40, 1.0, 0.0, b) for a, b in zip(r["x"].cpu().numpy(), r["u"].cpu().numpy())]
+        assert r["token"].tolist() == want
+
+
+def test_the_binding_s_two_ways_agree(mk, monkeypatch):
+    """The compiled way and the ctypes way: the same bits."""
+    g = gen(23)
+    lens = [70, 0, 9]
+    n = sum(lens)
+    q, k, v = (torch.randn(n, h, 64, generator=g, device="cuda").half() for h in (4, 2, 2))
+    cu, zero, x, u = ints(cu_of(lens)), ints([0, 0, 0]), noise(3, 999, 9), torch.rand(3, device="cuda")
+    status = ints([0])
+
+    def everything():
+        kc = torch.zeros(9, 2, 16, 64, device="cuda", dtype=torch.float16)
+        cache = mk.PagedKV(kc, kc.clone(), ints([[0, 1, 2, 3, 4], [8, 8, 8, 8, 8], [5, 8, 8, 8, 8]]))
+        qo, ko, out, o1 = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q), torch.empty_like(q[:3])
+        token = torch.zeros(3, dtype=torch.int32, device="cuda")
+        mk.kv_append(cache, q, k, v, cu, zero, 1e4, qo, ko, status=status)
+        mk.prompt_attention(qo, ko, v, cu, 70, out, status=status)
+        mk.paged_attention(cache, qo[:3], ints(lens), 70, o1, mk.paged_attention_workspace(cache, 4, 70), status=status)
+        mk.sample(x, u, token, torch.full((3,), 0.7, device="cuda"), ints([5, 0, 9]), torch.full((3,), 0.9, device="cuda"),
+                  torch.full((3,), 0.01, device="cuda"))
+        kv = cache.k.clone()
+        mk.kv_append(cache, None, k, v, cu, zero, 1e4)
+        return [qo, ko, out, o1, token, kv, cache.k, cache.v]
+
+    calls = []
+    real = mk._fast
+
+    class Counted:
+        def __getattr__(self, name):
+            def call(*a):
+                st = getattr(real, name)(*a)
+                calls.append((name, st))
+                return st
+            return call
+
+    class Never:
+        def __getattr__(self, name):
+            return lambda *a: -1
+
+    monkeypatch.setattr(mk, "_fast", Counted())
+    one = everything()
+    assert sorted(calls) == [("kv_append", 0), ("kv_append", 0), ("paged_attention", 0), ("prompt_attention", 0), ("sample", 0)]
+    monkeypatch.setattr(mk, "_fast", Never())
+    two = everything()
+    assert int(status) == 0
+    for a, b in zip(one, two):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_binding_refusals(mk):
+    g = gen(24)
+    cache = make_cache(mk, g, [40, 40], 2, 64, 16, torch.bfloat16)
+    ok = lambda *shape, dtype=torch.bfloat16: torch.zeros(*shape, device="cuda", dtype=dtype)
+    cu, st = ints([0, 1, 2]), ints([0, 0])
+    k, q = ok(2, 2, 64), ok(2, 4, 64)
+    ws = mk.paged_attention_workspace(cache, 4, 40)
+
+    def append(**kw):
+        a = dict(q=q.clone(), k=k.clone(), v=k.clone(), cu_tokens=cu, start_pos=st, rope_theta=1e4)
+        a.update(kw)
+        mk.kv_append(cache, **a)
+
+    def paged(**kw):
+        a = dict(q=q, kv_lens=st, max_len=40, out=q.clone(), workspace=ws)
+        a.update(kw)
+        mk.paged_attention(cache, **a)
+
+    def prompt(**kw):
+        a = dict(q=q, k=k, v=k, cu_seqlens=cu, max_len=2, out=q.clone())
+        a.update(kw)
+        mk.prompt_attention(**a)
+
+    def sample(**kw):
+        a = dict(logits=ok(2, 50, dtype=torch.float32), uniform=ok(2, dtype=torch.float32), token_out=ints([0, 0]))
+        a.update(kw)
+        mk.sample(**a)
+
+    append(), paged(), prompt(), sample()
+    bad = [(append, dict(k=k.half())), (append, dict(q=ok(2, 3, 64))), (append, dict(q=ok(3, 4, 64))), (append, dict(v=k.cpu())),
+           (append, dict(k=ok(2, 64, 2).transpose(1, 2))), (append, dict(cu_tokens=ints([0, 1]))),
+           (append, dict(cu_tokens=torch.zeros(3, dtype=torch.int64, device="cuda"))), (append, dict(rope_theta=0.5)),
+           (append, dict(q=None, q_out=q)), (append, dict(status=ints([0, 0]))), (append, dict(q_out=ok(2, 4, 128)[..., ::2])),
+           (append, dict(q=ok(2, 4 * 64 + 4)[:, 4:].unflatten(1, (4, 64)))),
+           (paged, dict(out=q.half())), (paged, dict(kv_lens=ints([0]))), (paged, dict(max_len=1000)), (paged, dict(max_len=-1)),
+           (paged, dict(workspace=ws[:8])), (paged, dict(workspace=ws.cpu())), (paged, dict(scale=0.0)), (paged, dict(q=ok(2, 20, 64), out=ok(2, 20, 64))),
+           (prompt, dict(k=ok(2, 3, 64), v=ok(2, 3, 64))), (prompt, dict(q=q.float())), (prompt, dict(out=ok(3, 4, 64))),
+           (prompt, dict(cu_seqlens=ints([0])[:0])), (prompt, dict(scale=-1.0)), (prompt, dict(q=ok(2, 4, 32), k=ok(2, 2, 32), v=ok(2, 2, 32), out=ok(2, 4, 32))),
+           (sample, dict(logits=ok(2, 50))), (sample, dict(logits=ok(2, 50, dtype=torch.float32).t())), (sample, dict(uniform=ok(3, dtype=torch.float32))),
+           (sample, dict(top_k=ok(2, dtype=torch.float32))), (sample, dict(token_out=torch.zeros(2, dtype=torch.int64, device="cuda"))),
+           (sample, dict(top_p=ok(4, dtype=torch.float32)[::2]))]
+    for f, kw in bad:
+        with pytest.raises(mk.MkError) as e:
+            f(**kw)
+        assert e.value.status == mk.MK_ERR_INVALID, kw
+    torch.cuda.synchronize()
+
+
 # ---- used together, and with the decode step ---------------------------------------------
 
 def test_prompt_then_decode_over_pages(mk):
@@ -795,3 +1003,54 @@ def test_operators_read_and_write_a_contexts_cache(mk, max_batch):
     before[max_batch - 1, :, n] = kc[last][max_batch - 1, :, n]
     assert torch.equal(kc[last], before)
     ctx.close()
+
+
+def test_decode_loop_in_one_graph(mk):
+    """A serving loop's step -- append, attend, project, sample -- captured once and replayed
+    while the positions grow and the sampled tokens feed the next step, as the same calls made
+    one by one."""
+    nq, nkv, d, page, vocab, seqs, steps = 4, 2, 64, 16, 500, 3, 20
+    g = gen(31)
+    table = ints([[s * 3 + i for i in range(3)] for s in range(seqs)])
+    wq, wk, wv, wo = (torch.randn(vocab, h * d, generator=g, device="cuda").bfloat16() for h in (nq, nkv, nkv, nq))
+    u = torch.rand(steps, seqs, generator=g, device="cuda")
+    kk, pp = ints([30] * seqs), torch.full((seqs,), 0.95, device="cuda")
+    one = ints([0, 1, 2, 3])
+
+    def loop(graph):
+        kc = torch.zeros(9, nkv, page, d, device="cuda", dtype=torch.bfloat16)
+        cache = mk.PagedKV(kc, kc.clone(), table)
+        token, pos, lens, un = ints([1, 2, 3]), ints([0, 5, 11]), ints([1, 6, 12]), torch.zeros(seqs, device="cuda")
+        out = torch.empty(seqs, nq, d, device="cuda", dtype=torch.bfloat16)
+        ws = mk.paged_attention_workspace(cache, nq, 3 * page)
+
+        def step():
+            t = token.long()
+            q, k, v = wq[t].view(seqs, nq, d).clone(), wk[t].view(seqs, nkv, d), wv[t].view(seqs, nkv, d)
+            mk.kv_append(cache, q, k, v, one, pos, 1e4)
+            mk.paged_attention(cache, q, lens, 3 * page, out, ws)
+            mk.sample(out.view(seqs, -1).float() @ wo.float().t(), un, token, None, kk, pp)
+            pos.add_(1)
+            lens.add_(1)
+
+        if graph:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(2):
+                    step()
+            torch.cuda.synchronize()
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr, stream=st):
+                step()
+            kc.zero_(), cache.v.zero_()
+            token.copy_(ints([1, 2, 3])), pos.copy_(ints([0, 5, 11])), lens.copy_(ints([1, 6, 12]))
+        seen = []
+        for i in range(steps):
+            un.copy_(u[i])
+            gr.replay() if graph else step()
+            seen.append(token.clone())
+        torch.cuda.synchronize()
+        return torch.stack(seen), cache.k.clone(), cache.v.clone()
+
+    for a, b in zip(loop(False), loop(True)):
+        assert torch.equal(a, b)
