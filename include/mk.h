@@ -590,7 +590,8 @@ int mk_kv_append(const mk_paged_kv *kv, const int32_t *cu_tokens, const int32_t 
  *             sizes the launch and the workspace, so that the same launch can
  *             be replayed while the lengths grow up to it.  n_seqs *
  *             n_kv_heads * (max_len + 512) is below 2^34.
- *   q, out    [n_seqs][n_q_heads][head_dim], the cache's dtype
+ *   q, out    [n_seqs][n_q_heads][head_dim], the cache's dtype; out may be q
+ *             (with its stride), and overlaps nothing else
  *   scale     > 0; usually 1 / sqrt(head_dim)
  *   workspace device, 16-byte aligned, at least the bytes
  *             mk_paged_attention_workspace reports, filled with zeros once
@@ -606,8 +607,7 @@ int mk_paged_attention(const mk_paged_kv *kv, const int32_t *kv_lens, int max_le
                        size_t workspace_bytes, int32_t *status_out, mk_stream_t stream);
 
 /* Bytes of workspace mk_paged_attention needs on the current device for
- * these sizes (*bytes_out; 0 is possible, the workspace may then be NULL).
- * The pointers of *kv are not looked at. */
+ * these sizes (*bytes_out).  The pointers of *kv are not looked at. */
 int mk_paged_attention_workspace(const mk_paged_kv *kv, int max_len, int n_q_heads, size_t *bytes_out);
 
 /*
@@ -656,7 +656,7 @@ int mk_prompt_attention(int dtype, int n_q_heads, int n_kv_heads, int head_dim, 
  *                largest.  NULL: off.
  *   min_p        device float [rows]; not above 0: off; above 1 counts as 1.
  *                NULL: off.
- *   token_out    device int32 [rows]
+ *   token_out    device int32 [rows], overlapping none of the inputs
  * Logits of -infinity and NaN are never chosen; a row with nothing else gives
  * -1 (which mk_decode_step refuses).  +infinity takes all the weight, shared
  * among its equals.

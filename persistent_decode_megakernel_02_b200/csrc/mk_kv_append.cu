@@ -124,7 +124,7 @@ void go(const AppendParams &p, int num_sms, cudaStream_t stream) {
     // ones: 9.5, 7.9, 8.4, 9.8; 16: 3.2, 3.4, 3.9, 5.2).
     const int n = p.a.n_tokens;
     if (n <= 4 * num_sms) kv_append_kernel<T, D, 1><<<n, kAppendThreads, 0, stream>>>(p);
-    else kv_append_kernel<T, D, 2><<<(n + 1) / 2, kAppendThreads, 0, stream>>>(p);
+    else kv_append_kernel<T, D, 2><<<n / 2 + n % 2, kAppendThreads, 0, stream>>>(p);
 }
 
 }  // namespace

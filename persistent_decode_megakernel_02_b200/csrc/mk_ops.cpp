@@ -133,7 +133,7 @@ int mk_paged_attention(const mk_paged_kv *kv, const int32_t *kv_lens, int max_le
     const int st = ops_device(&dev, &sms);
     if (st != MK_OK) return st;
     const size_t need = paged_workspace(*kv, max_len, n_q_heads, sms);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return MK_ERR_INVALID;
+    if (!workspace || workspace_bytes < need) return MK_ERR_INVALID;
     PagedArgs a{*kv, kv_lens, max_len, n_q_heads, q, out, q_stride, out_stride, scale, workspace, status_out};
     return launched(paged_launch(a, dev, sms, (cudaStream_t)stream));
 }

@@ -161,10 +161,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
         }
         return (len + kTile * R - 1) / (kTile * R);
     };
-    auto count = [&](int level) {       // sequences that have it
-        int c = 0;
-        for (int s0 = 0; s0 < a.n_seqs; s0 += 32)
-            c += __popc(__ballot_sync(0xffffffffu, levels_of(s0 + lane) > level));
+    // sequences that have a level; down to level `low` they are the same, so
+    // the lengths are read once per different number of levels
+    int low = 0;
+    auto count = [&](int level) {
+        int c = 0, shorter = 0;
+        for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
+            const int levels = levels_of(s0 + lane);
+            c += __popc(__ballot_sync(0xffffffffu, levels > level));
+            if (levels <= level) shorter = max(shorter, levels);
+        }
+        low = __reduce_max_sync(0xffffffffu, shorter);
         return c;
     };
     int level = 0, here = 0;
@@ -182,7 +189,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
     if (warp >= 8) set_regs_down<kControlRegsPrompt>();
     if (warp == 8) {
         // ---- scheduler and loader
-        long long base = 0;                               // items before it
+        long long base = 0;                               // items before the level
+        int at = 0, passed = 0;      // the level's sequences before sequence `at`: the search goes on from there
         const int P = gridDim.x;
         int k = 0, F = 0;     // items published, tiles loaded
         bool ok = true;
@@ -191,24 +199,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
             while (level >= 0 && rank >= base + (long long)here * per_seq) {
                 base += (long long)here * per_seq;
                 --level;
-                here = level >= 0 ? count(level) : 0;
+                at = passed = 0;
+                if (level < low) here = level >= 0 ? count(level) : 0;
             }
             PromptItem it;
             it.row0 = it.len = it.kvh = it.tiles = 0;
             for (int u = 0; u < 2; ++u) it.blk[u] = it.head[u] = it.n[u] = 0;
             if (level >= 0) {
-                int nth = (int)((rank - base) / per_seq);
+                const int nth = (int)((rank - base) / per_seq);
                 const int rem = (int)((rank - base) % per_seq);
                 it.kvh = rem % a.nkv;
-                for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
-                    const unsigned m = __ballot_sync(0xffffffffu, levels_of(s0 + lane) > level);
-                    if (nth < __popc(m)) {
-                        const int src = __fns(m, 0, nth + 1);
+                for (; at < a.n_seqs; at += 32) {
+                    const unsigned m = __ballot_sync(0xffffffffu, levels_of(at + lane) > level);
+                    if (nth < passed + __popc(m)) {
+                        const int src = __fns(m, 0, nth - passed + 1);
                         it.row0 = __shfl_sync(0xffffffffu, row0, src);
                         it.len = __shfl_sync(0xffffffffu, len, src);
                         break;
                     }
-                    nth -= __popc(m);
+                    passed += __popc(m);
                 }
                 const int blocks = (it.len + kTile - 1) / kTile;
                 for (int u = 0; u < 2; ++u) {

@@ -973,7 +973,10 @@ cudaError_t sample_launch(const SampleArgs &a, int device, int num_sms, cudaStre
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sample_kernel, a, steps, a.top_p && (long long)a.rows * cluster > 2 * num_sms);
+    // every cluster looks the order up for itself: up to 1024 rows, beyond which
+    // the last rows are little of the whole
+    const bool in_order = a.top_p && (long long)a.rows * cluster > 2 * num_sms && a.rows <= 1024;
+    return cudaLaunchKernelEx(&cfg, sample_kernel, a, steps, in_order);
 }
 
 }  // namespace mk

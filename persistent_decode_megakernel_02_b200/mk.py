@@ -10,6 +10,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes as C
+import operator
 import os
 import re
 
@@ -397,6 +398,17 @@ def _invalid(what: str, why: str):
     raise MkError(MK_ERR_INVALID, f"{what}: {why}")
 
 
+def _ints(what: str, **numbers):
+    """Numbers the library takes as ints: ctypes would drop their upper bits."""
+    for name, n in numbers.items():
+        try:
+            fits = -(1 << 31) <= operator.index(n) < 1 << 31
+        except TypeError:
+            fits = False
+        if not fits:
+            _invalid(what, f"{name} = {n} is no 32-bit number")
+
+
 def _dtype_code(dtype) -> int:
     return MK_BF16 if dtype is torch.bfloat16 else MK_FP16 if dtype is torch.float16 else -1
 
@@ -457,6 +469,8 @@ class PagedKV:
         if (page_table.dim() != 2 or page_table.dtype is not torch.int32 or page_table.device != k.device
                 or not page_table.is_contiguous()):
             _invalid(what, "page_table must be a contiguous int32 [n_seqs][pages_per_seq] on k's device")
+        _ints(what, n_seqs=page_table.shape[0], pages_per_seq=page_table.shape[1], num_pages=k.shape[0],
+              n_kv_heads=k.shape[1], page_size=k.shape[2], head_dim=k.shape[3])
         self.k, self.v, self.page_table = k, v, page_table
         self.dtype, self.device, self.dev = k.dtype, k.device, k.get_device()
         self.n_seqs, self.pages_per_seq = page_table.shape
@@ -497,6 +511,7 @@ def kv_append(cache: PagedKV, q, k, v, cu_tokens, start_pos, rope_theta: float, 
     if k_out is not None:
         kos = _rows(what, "k_out", k_out, dt, dev, shape)
         kop = k_out.data_ptr()
+    _ints(what, tokens=n, n_q_heads=nq)
     cu = _vec(what, "cu_tokens", cu_tokens, i32, dev, cache.n_seqs + 1)
     sp = _vec(what, "start_pos", start_pos, i32, dev, cache.n_seqs)
     if n == 0:
@@ -510,6 +525,7 @@ def paged_attention_workspace(cache: PagedKV, n_q_heads: int, max_len: int):
     """A workspace for paged_attention calls of these sizes (zero-filled uint8
     CUDA tensor; calls that may overlap on the device need one each)."""
     n = C.c_size_t()
+    _ints("paged_attention_workspace", max_len=max_len, n_q_heads=n_q_heads)
     with torch.cuda.device(cache.dev):
         _check(_lib.mk_paged_attention_workspace(cache._ref, max_len, n_q_heads, C.byref(n)),
                "mk_paged_attention_workspace")
@@ -529,6 +545,7 @@ def paged_attention(cache: PagedKV, q, kv_lens, max_len: int, out, workspace=Non
         return
     what, dev, dt, i32 = "paged_attention", cache.dev, cache.dtype, torch.int32
     nq = q.shape[1] if q.dim() == 3 else 0
+    _ints(what, max_len=max_len, n_q_heads=nq)
     shape = (cache.n_seqs, nq, d)
     qs = _rows(what, "q", q, dt, dev, shape)
     os_ = _rows(what, "out", out, dt, dev, shape)
@@ -556,6 +573,7 @@ def prompt_attention(q, k, v, cu_seqlens, max_len: int, out, scale=None, status=
         _invalid(what, "q and k must be [n][heads][d] CUDA tensors of bf16 or fp16, cu_seqlens a vector")
     n, nq, d = q.shape
     nkv, ns = k.shape[1], cu_seqlens.shape[0] - 1
+    _ints(what, tokens=n, n_q_heads=nq, n_kv_heads=nkv, head_dim=d, n_seqs=ns, max_len=max_len)
     kshape = (n, nkv, d)
     qs = _rows(what, "q", q, dt, dev, (n, nq, d))
     ks = _rows(what, "k", k, dt, dev, kshape)
@@ -579,6 +597,7 @@ def sample(logits, uniform, token_out, temperature=None, top_k=None, top_p=None,
     if logits.dim() != 2 or logits.dtype is not f or dev < 0:
         _invalid(what, "logits must be a float32 CUDA tensor [rows][vocab]")
     rows, vocab = logits.shape
+    _ints(what, rows=rows, vocab=vocab)
     st = logits.stride()
     if vocab > 1 and st[1] != 1:
         _invalid(what, "rows of logits must be contiguous")

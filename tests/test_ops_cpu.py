@@ -146,6 +146,13 @@ def test_cache_struct_matches_the_c_compiler(tmp_path):
     assert got == want + [mk.MAX_GROUP, mk.MAX_VOCAB]
 
 
+@pytest.mark.parametrize("n", [1 << 31, (1 << 32) + 5, -(1 << 31) - 1, 1.0, None, "4"])
+def test_binding_numbers_that_are_no_int(n):
+    with pytest.raises(mk.MkError) as e:      # ctypes alone would make 5 of the second
+        mk._ints("call", fine=(1 << 31) - 1, max_len=n)
+    assert e.value.status == mk.MK_ERR_INVALID and "max_len" in str(e.value)
+
+
 def test_binding_checks_its_tensors():
     import torch
     k = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)

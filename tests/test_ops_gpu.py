@@ -738,6 +738,8 @@ def test_sample_many_rows(mk):
     k = [int(v) for v in rng.choice([0, 0, 5, 40], rows)]
     p = [float(v) for v in rng.choice([1.0, 0.6, 0.9], rows)]
     sample_case(mk, noise(rows, 3001, 14), k=k, p=p)
+    # more rows than are put in order
+    sample_case(mk, noise(3 * rows, 301, 15), k=3 * k, p=3 * p)
 
 
 # ---- workspaces, shared pages, streams, both ways of the binding ------------------------
@@ -776,6 +778,16 @@ def test_paged_nothing_or_next_to_nothing(mk, lens, max_len):
     paged_case(mk, lens, 4, 2, 64, 16, torch.bfloat16, max_len=max_len)
 
 
+def test_paged_in_place(mk):
+    g = gen(25)
+    lens = [3000, 17, 0, 900]
+    cache = make_cache(mk, g, lens, 2, 128, 16, torch.bfloat16)
+    q = torch.randn(4, 8, 128, generator=g, device="cuda").bfloat16()
+    out = q.clone()
+    mk.paged_attention(cache, out, ints(lens), 3000, out)
+    paged_check(cache, q, lens, out, 128 ** -0.5)
+
+
 def test_paged_max_len_beyond_the_table(mk):
     # one page of 16 a sequence: 50 tokens cannot be there
     with pytest.raises(mk.MkError) as e:
@@ -788,6 +800,54 @@ def test_prompt_many_sequences(mk):
     lens = [int(x) for x in rng.integers(0, 300, 200)]
     prompt_case(mk, lens, 4, 1, 64, torch.bfloat16, seed=1)
     prompt_case(mk, lens[:70], 3, 1, 128, torch.float16, seed=2)
+
+
+def test_prompt_long_and_many_short(mk):
+    # levels with one sequence, with few and with all of them, beyond 32 at a time
+    rng = np.random.default_rng(2)
+    lens = [int(x) for x in rng.integers(0, 140, 90)] + [2100] + [int(x) for x in rng.integers(0, 700, 40)] + [1, 0, 1290]
+    prompt_case(mk, lens, 2, 1, 64, torch.bfloat16, seed=3)
+    prompt_case(mk, lens, 3, 1, 64, torch.float16, seed=4)
+
+
+def test_first_calls_of_a_process_are_captured():
+    """Nothing an operator sets up at its first call is forbidden in a capture."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from persistent_decode_megakernel_02_b200 import mk
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+kc = torch.zeros(9, 2, 16, 64, device="cuda", dtype=torch.bfloat16)
+cache = mk.PagedKV(kc, kc.clone(), i([[0, 1, 2, 3]]))
+q, k, v = (torch.randn(60, h, 64, device="cuda").bfloat16() for h in (4, 2, 2))
+cu, zero, lens, x, u = i([0, 60]), i([0]), i([60]), torch.randn(3, 999, device="cuda"), torch.rand(3, device="cuda")
+qo, ko, out, o1, token = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q), torch.empty_like(q[:1]), i([0, 0, 0])
+ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+def run():
+    mk.kv_append(cache, q, k, v, cu, zero, 1e4, qo, ko)
+    mk.prompt_attention(qo, ko, v, cu, 60, out)
+    mk.paged_attention(cache, qo[59:], lens, 60, o1, ws)
+    mk.sample(x, u, token)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (qo, ko, out, o1, token)]
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (qo, ko, out, o1, token)))
+# the last prompt row and the one-token form see the same keys: both round their
+# result once, the prompt form its weights too (bf16, half a step: 2^-9 each)
+d = (out[59:].float() - o1.float()).abs().max()
+assert d <= 3 * 2.0 ** -8 * v.float().abs().max(), d
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_calls_at_once_on_two_streams(mk):
@@ -906,6 +966,8 @@ def test_binding_refusals(mk):
            (append, dict(q=None, q_out=q)), (append, dict(status=ints([0, 0]))), (append, dict(q_out=ok(2, 4, 128)[..., ::2])),
            (append, dict(q=ok(2, 4 * 64 + 4)[:, 4:].unflatten(1, (4, 64)))),
            (paged, dict(out=q.half())), (paged, dict(kv_lens=ints([0]))), (paged, dict(max_len=1000)), (paged, dict(max_len=-1)),
+           (paged, dict(max_len=(1 << 32) + 5)), (paged, dict(max_len=(1 << 32) + 5, workspace=None)), (prompt, dict(max_len=(1 << 32) + 5)),
+           (prompt, dict(max_len=-1)), (prompt, dict(max_len=2.5)),
            (paged, dict(workspace=ws[:8])), (paged, dict(workspace=ws.cpu())), (paged, dict(scale=0.0)), (paged, dict(q=ok(2, 20, 64), out=ok(2, 20, 64))),
            (prompt, dict(k=ok(2, 3, 64), v=ok(2, 3, 64))), (prompt, dict(q=q.float())), (prompt, dict(out=ok(3, 4, 64))),
            (prompt, dict(cu_seqlens=ints([0])[:0])), (prompt, dict(scale=-1.0)), (prompt, dict(q=ok(2, 4, 32), k=ok(2, 2, 32), v=ok(2, 2, 32), out=ok(2, 4, 32))),
