@@ -420,21 +420,45 @@ __device__ __forceinline__ u64 reg_block_scan(u64 v, u64 *tmp, u64 &total) {
 
 // With more rows than fit the device at once, those with top-p alone, which
 // take about twice as long, come first: the row of cluster c in that order.
+// Every cluster looks it up for itself, so only up to kOrderRows rows, whose
+// parameters are a few loads side by side; with more the last rows are little
+// of the whole.  64 rows of 151936 with eight slow ones last: 68.7 us in the
+// rows' own order, 57.4 in this one; 128: 140 and 122; no slow ones among 128
+// (what the look-up costs): 82 and 85.  Up to 256 rows: 132 and 95 at 128.
+constexpr int kOrderRows = 128;
 __device__ __forceinline__ int row_in_order(const SampleArgs &a, int c) {
     const int lane = threadIdx.x & 31;
-    auto slow = [&](int r) {
-        if (r >= a.rows || !(a.top_p[r] < 1.f)) return false;
-        const int k = a.top_k ? a.top_k[r] : 0;
-        return !(k > 0 && k < a.vocab);
-    };
+    float p[kOrderRows / 32];
+    int k[kOrderRows / 32];
+#pragma unroll
+    for (int i = 0; i < kOrderRows / 32; ++i) {
+        const int r = i * 32 + lane;
+        p[i] = r < a.rows ? a.top_p[r] : 1.f;
+        k[i] = r < a.rows && a.top_k ? a.top_k[r] : 0;
+    }
+    unsigned slow[kOrderRows / 32];
+#pragma unroll
+    for (int i = 0; i < kOrderRows / 32; ++i)
+        slow[i] = __ballot_sync(0xffffffffu, p[i] < 1.f && !(k[i] > 0 && k[i] < a.vocab));
+    int row0 = 0, nth = 0;      // the nth of `among`, rows from row0
+    unsigned among = 1;
+#pragma unroll
     for (int pass = 0; pass < 2; ++pass)
-        for (int r0 = 0; r0 < a.rows; r0 += 32) {
-            const bool mine = slow(r0 + lane) == (pass == 0) && r0 + lane < a.rows;
-            const unsigned m = __ballot_sync(0xffffffffu, mine);
-            if (c < __popc(m)) return r0 + __fns(m, 0, c + 1);
-            c -= __popc(m);
+#pragma unroll
+        for (int i = 0; i < kOrderRows / 32; ++i) {
+            const int there = min(a.rows - i * 32, 32);
+            if (there <= 0) break;
+            const unsigned m = (pass == 0 ? slow[i] : ~slow[i]) & (there == 32 ? 0xffffffffu : (1u << there) - 1);
+            const int n = __popc(m);
+            if (c >= 0 && c < n) {
+                row0 = i * 32;
+                nth = c;
+                among = m;
+            }
+            c -= n;
         }
-    return 0;      // not reached: every row is one or the other
+    const bool me = (among >> lane & 1u) && __popc(among & ((1u << lane) - 1)) == nth;
+    return row0 + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
 }
 
 // A block's slice of the row is 16 warps\' parts of IT vector steps (4 logits a
@@ -973,9 +997,7 @@ cudaError_t sample_launch(const SampleArgs &a, int device, int num_sms, cudaStre
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    // every cluster looks the order up for itself: up to 1024 rows, beyond which
-    // the last rows are little of the whole
-    const bool in_order = a.top_p && (long long)a.rows * cluster > 2 * num_sms && a.rows <= 1024;
+    const bool in_order = a.top_p && (long long)a.rows * cluster > 2 * num_sms && a.rows <= kOrderRows;
     return cudaLaunchKernelEx(&cfg, sample_kernel, a, steps, in_order);
 }
 
