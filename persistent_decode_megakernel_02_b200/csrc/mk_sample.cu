@@ -336,10 +336,12 @@ struct RegShared {
             float maxima[kMaxCluster * kRegThreads];
             uint32_t bins[kBins];
         };
+        struct {                      // block 0, once all have gathered: the above is read by then
+            u64 sorted[kListMax];
+            ulonglong2 kept[kListMax];
+        };
     };
     u64 list[kListMax];               // gathered logits: key, then lowest index first
-    u64 sorted[kListMax];
-    ulonglong2 kept[kListMax];
     u64 sub[kRegWarps];
     double table[32];
     // written by every block of the cluster, read by all
