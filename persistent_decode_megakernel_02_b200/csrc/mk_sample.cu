@@ -48,22 +48,25 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 
 // Weights of a row.  2^(y / 32) for y = 32 (x - top) / (T ln 2) <= 0, as 2^n
 // 2^(i / 32) 2^(r / 32): i from a table of 32, and |r| <= 1/2 by the Taylor
-// polynomial of degree 4 (relative error (ln 2 / 64)^5 / 120 < 1.3e-12).  Ten
-// 64-bit operations; the library's exp() made the passes that weigh a whole
-// row twice as long.
+// polynomial of degree 4 (relative error (ln 2 / 64)^5 / 120 < 1.3e-12).
+// Eleven 64-bit operations and no branch; the library's exp() made the passes
+// that weigh a whole row twice as long.
 constexpr double kMagic = 6755399441055744.0;     // 1.5 * 2^52: adding it rounds to an integer
-constexpr double kTwo52 = 4503599627370496.0;
+constexpr double kTwo52 = 4503599627370496.0;     // the same, and a value below 2^52 becomes the low bits
+constexpr u64 kTwo52Bits = 0x4330000000000000ull;
 constexpr double kUnit = 8796093022208.0;         // 2^43
 constexpr double kC = 0.021660849392498290;       // ln 2 / 32
 struct Weight {
-    double c32, off, min_v;      // y = c32 x - off; min_v: min-p, in units
-    float top, reach, floor;     // logits below `reach` weigh nothing, below `floor` nothing in the final choice
+    double c32, top_d, min_v;    // y = c32 (x - top_d); min_v: min-p, in units
+    // Logits below `reach` weigh nothing, below `floor` nothing in the final
+    // choice; both are finite, so that -infinity is below them.
+    float cap, reach, floor;
     const double *table;         // 2^(i / 32), shared memory
 
-    __device__ __forceinline__ void init(const SampleArgs &a, int row, float top_, float t, const double *tab) {
+    __device__ __forceinline__ void init(const SampleArgs &a, int row, float top, float t, const double *tab) {
         c32 = 46.166241308446828384 / (double)t;  // 32 / ln 2
-        top = top_;
-        off = (double)top * c32;
+        cap = top == INFINITY ? 0.f : top;        // an infinite top and its equals weigh one
+        top_d = (double)cap;
         float far = 31.2f;       // e^-31.2 < 2^-45
         const float mp = a.min_p ? a.min_p[row] : 0.f;
         min_v = 0.0;
@@ -71,14 +74,15 @@ struct Weight {
             min_v = fmin((double)mp, 1.0) * kUnit;
             far = fminf(far, fmaxf(-logf(mp), 0.f) * 1.0001f + 1e-4f);
         }
-        reach = top - 31.2f * t;
-        floor = top - far * t;
+        const float lowest = -3.402823466e+38f;
+        reach = fmaxf(top - 31.2f * t, lowest);
+        floor = fmaxf(top - far * t, lowest);
         table = tab;
     }
-    // 2^43 w, before rounding; 0 below half a unit, and for -infinity.  No
-    // branches: four of these run side by side in every pass.
+    // 2^43 w, before rounding, of a logit that is not below `reach` (one that
+    // is weighs less than half a unit)
     __device__ __forceinline__ double scaled(float x) const {
-        const double y = fma((double)x, c32, -off);
+        const double y = ((double)fminf(fmaxf(x, reach), cap) - top_d) * c32;
         const double shifted = y + kMagic;
         const int n = __double2loint(shifted);
         const double d = y - (shifted - kMagic);
@@ -87,18 +91,20 @@ struct Weight {
         e = fma(d, e, kC);
         e = fma(d, e, 1.0);
         const double w = table[n & 31] * e;
-        const double v = __hiloint2double(__double2hiint(w) + (((n >> 5) + 43) << 20), __double2loint(w));
-        return x == top ? kUnit : x >= reach && x > -INFINITY ? v : 0.0;
+        return __hiloint2double(__double2hiint(w) + (((n >> 5) + 43) << 20), __double2loint(w));
     }
-    __device__ __forceinline__ u64 units(double v) const {      // v <= 2^43
-        return (u64)__double_as_longlong(v + kTwo52) & 0xfffffffffffffull;
+    // the weight in units, plus kTwo52Bits
+    __device__ __forceinline__ u64 units_raw(double v) const {      // v <= 2^43
+        return (u64)__double_as_longlong(v + kTwo52);
     }
-    __device__ __forceinline__ u64 whole(float x) const { return units(scaled(x)); }
+    __device__ __forceinline__ u64 whole(float x) const {
+        return x < reach ? 0ull : units_raw(scaled(x)) - kTwo52Bits;
+    }
     __device__ __forceinline__ bool enough(float x) const { return scaled(x) >= min_v; }
     // the weight in the final choice
     __device__ __forceinline__ u64 final_whole(float x) const {
         const double v = scaled(x);
-        return v >= min_v ? units(v) : 0;
+        return x < floor || v < min_v ? 0ull : units_raw(v) - kTwo52Bits;
     }
 };
 __device__ __forceinline__ void fill_table(double *table) {
@@ -178,7 +184,7 @@ __global__ void __launch_bounds__(kSampThreads) sample_long_kernel(SampleArgs a)
     const uint32_t top_key = (uint32_t)(best >> 32);
     Weight wt;
     wt.init(a, row, key_logit(top_key), t, sh.table);
-    const bool inf_top = isinf(wt.top);
+    const bool inf_top = top_key == 0xff800000u;
     // an infinite top leaves only its equals
     uint32_t cut = inf_top ? top_key : 1u;    // keys below are out
     uint32_t ties = 0xffffffffu;              // of keys equal to cut, this many (lowest indices) stay
@@ -342,7 +348,7 @@ struct RegShared {
         };
     };
     u64 list[kListMax];               // gathered logits: key, then lowest index first
-    u64 sub[kRegWarps];
+    u64 sub[kRegWarps], step[kMaxIt], groups[kBins / 32];
     double table[32];
     // written by every block of the cluster, read by all
     u64 x_best[kMaxCluster], x_sum[kMaxCluster], x_mass[kMaxCluster];
@@ -648,7 +654,7 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
 
     // Kept so far: logits above `cut`, and those equal to it up to index
     // `last`.  An infinite top leaves only its equals.
-    float cut = top == INFINITY ? INFINITY : -INFINITY;
+    float cut = top == INFINITY ? INFINITY : -3.402823466e+38f;      // (-infinity is out)
     int32_t last = 0x7fffffff;
 
     // The histogram bins of all blocks (filled, not yet synchronised): the
@@ -743,10 +749,11 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
         // registers
         u64 rest = 0;
         each([&](float f, int) {
+            if (f < wt.reach) return;
             const int b = bin_of(f);
-            const u64 w = wt.whole(f);
+            const u64 w = wt.units_raw(wt.scaled(f)) - kTwo52Bits;
             if (b == kBins - 1) rest += w;
-            else if (w) {
+            else {
                 atomicAdd(&sh.part[0][b], (uint32_t)w & 0x7fffu);
                 atomicAdd(&sh.part[1][b], (uint32_t)(w >> 15) & 0x3fffu);
                 atomicAdd(&sh.part[2][b], (uint32_t)(w >> 29));
@@ -754,48 +761,54 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
         });
         rest = reg_block_sum(rest, sh.tmp64);
         if (tid < CL) cl.map_shared_rank(&sh, tid)->x_sum[rank] = rest;
-        // the parts together, four consecutive bins a thread, then over the
-        // blocks: every block finds the bin by itself
-        u64 m[4], msum = 0;
+        // The parts together, four consecutive bins a thread, and the sums of
+        // groups of 32 bins.  Every block finds the group over all blocks, then
+        // the bin in it, by itself (reading all blocks' bins took 15300 cycles
+        // of the 69000 of one row).
         {
             const uint4 p0 = reinterpret_cast<const uint4 *>(sh.part[0])[tid], p1 = reinterpret_cast<const uint4 *>(sh.part[1])[tid],
                         p2 = reinterpret_cast<const uint4 *>(sh.part[2])[tid];
-            m[0] = p0.x + ((u64)p1.x << 15) + ((u64)p2.x << 29);
-            m[1] = p0.y + ((u64)p1.y << 15) + ((u64)p2.y << 29);
-            m[2] = p0.z + ((u64)p1.z << 15) + ((u64)p2.z << 29);
-            m[3] = p0.w + ((u64)p1.w << 15) + ((u64)p2.w << 29);
+            const u64 m0 = p0.x + ((u64)p1.x << 15) + ((u64)p2.x << 29), m1 = p0.y + ((u64)p1.y << 15) + ((u64)p2.y << 29),
+                      m2 = p0.z + ((u64)p1.z << 15) + ((u64)p2.z << 29), m3 = p0.w + ((u64)p1.w << 15) + ((u64)p2.w << 29);
+            __syncthreads();
+            reinterpret_cast<ulonglong2 *>(sh.sums)[2 * tid] = make_ulonglong2(m0, m1);
+            reinterpret_cast<ulonglong2 *>(sh.sums)[2 * tid + 1] = make_ulonglong2(m2, m3);
+            u64 group = m0 + m1 + m2 + m3;
+            for (int o = 1; o < 8; o <<= 1) group += __shfl_xor_sync(0xffffffffu, group, o);
+            if ((tid & 7) == 0) sh.groups[tid >> 3] = group;
         }
-        __syncthreads();
-        reinterpret_cast<ulonglong2 *>(sh.sums)[2 * tid] = make_ulonglong2(m[0], m[1]);
-        reinterpret_cast<ulonglong2 *>(sh.sums)[2 * tid + 1] = make_ulonglong2(m[2], m[3]);
         if (tid == 0) sh.found_bin = 0xffffffffu;
         cl.sync();
-#pragma unroll
-        for (int r = 1; r < kMaxCluster; ++r)
-            if (r < CL) {
-                const ulonglong2 *o = reinterpret_cast<const ulonglong2 *>(cl.map_shared_rank(&sh, (rank + r) % CL)->sums);
-                const ulonglong2 o0 = o[2 * tid], o1 = o[2 * tid + 1];
-                m[0] += o0.x;
-                m[1] += o0.y;
-                m[2] += o1.x;
-                m[3] += o1.y;
-            }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) msum += m[i];
+        // the sum over the blocks of entry tid / 8, in all eight threads of it
+        auto over_blocks = [&](auto entry_of) {
+            u64 v = 0;
+            const int b = tid & 7;
+            if (b < CL) v = entry_of(cl.map_shared_rank(&sh, b));
+            for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            return v;
+        };
+        const u64 group = over_blocks([&](const RegShared *o) { return o->groups[tid >> 3]; });
         u64 all;
-        u64 at = reg_block_scan(msum, sh.tmp64, all);
+        const u64 group_at = reg_block_scan(tid & 7 ? 0 : group, sh.tmp64, all);      // exclusive: right in the first of eight
         for (int r = 0; r < CL; ++r) all += sh.x_sum[r];
         const double target = (double)p * (double)all;
         auto reached = [&](u64 mass) { return mass > 0 && (double)mass >= target; };    // the top is in bin 0
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (!reached(at) && reached(at + m[i])) {
-                sh.found_bin = 4 * tid + i;
-                sh.found_mass = at;
-            }
-            at += m[i];
+        if ((tid & 7) == 0 && !reached(group_at) && reached(group_at + group)) {
+            sh.found_bin = tid >> 3;
+            sh.found_mass = group_at;
         }
         __syncthreads();
+        const uint32_t in_group = sh.found_bin;
+        if (in_group != 0xffffffffu) {
+            const u64 mass = over_blocks([&](const RegShared *o) { return tid < 256 ? o->sums[in_group * 32 + (tid >> 3)] : 0; });
+            u64 sum;
+            const u64 at = sh.found_mass + reg_block_scan(tid & 7 ? 0 : mass, sh.tmp64, sum);      // synchronises
+            if (tid < 256 && (tid & 7) == 0 && !reached(at) && reached(at + mass)) {
+                sh.found_bin = in_group * 32 + (tid >> 3);
+                sh.found_mass = at;
+            }
+            __syncthreads();
+        }
         if (sh.found_bin != 0xffffffffu) {
             const int bin = (int)sh.found_bin;
             each([&](float f, int i) {
@@ -855,44 +868,55 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
         __syncthreads();
         if (lane == 0) sh.sub[warp] = s;
         __syncthreads();
-        u64 mine = 0, warp_before = 0;
+        u64 mine = 0;
 #pragma unroll
-        for (int w = 0; w < kRegWarps; ++w) {
-            if (w == warp) warp_before = mine;
-            mine += sh.sub[w];
-        }
+        for (int w = 0; w < kRegWarps; ++w) mine += sh.sub[w];
         if (tid < CL) cl.map_shared_rank(&sh, tid)->x_sum[rank] = mine;
         cl.sync();
-        u64 total = 0, before = 0;
+        u64 total = 0, run = 0;
         for (int r = 0; r < CL; ++r) {
-            if (r == rank) before = total;
+            if (r == rank) run = total;
             total += sh.x_sum[r];
         }
         const u64 g = goal(total);
-        u64 run = before + warp_before;
-        if (g < run || g >= run + s) return;       // the same answer for the whole warp
-        for (int it = 0; it < IT; ++it) {
-            const float4 q = xs[it * kRegThreads + tid];
-            const int i = base + it * 128;
-            const u64 w[4] = {weight(q.x, i), weight(q.y, i + 1), weight(q.z, i + 2), weight(q.w, i + 3)};
-            const u64 own = w[0] + w[1] + w[2] + w[3];
-            u64 at = own;
+        if (g < run || g >= run + mine) return;       // not in this block
+        // the warp's part that holds it; its steps are weighed by a warp each
+        // (by the part's own warp, one step after another, it took 8000 cycles)
+        int part = 0;
+#pragma unroll
+        for (int w = 0; w < kRegWarps - 1; ++w)
+            if (part == w && g >= run + sh.sub[w]) {
+                run += sh.sub[w];
+                part = w + 1;
+            }
+        const int first = rank * IT * kVecStep + part * IT * 128 + lane * 4 - skew;
+        u64 own[4];
+        auto step_sum = [&](int it) {       // up to and with this lane
+            const float4 q = xs[it * kRegThreads + part * 32 + lane];
+            const int i = first + it * 128;
+            own[0] = weight(q.x, i);
+            own[1] = weight(q.y, i + 1);
+            own[2] = weight(q.z, i + 2);
+            own[3] = weight(q.w, i + 3);
+            u64 at = own[0] + own[1] + own[2] + own[3];
             for (int o = 1; o < 32; o <<= 1) {
                 const u64 y = __shfl_up_sync(0xffffffffu, at, o);
                 if (lane >= o) at += y;
             }
-            const u64 all = __shfl_sync(0xffffffffu, at, 31);
-            if (g >= run + all) {
-                run += all;
-                continue;
-            }
-            at += run - own;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (g >= at && g < at + w[c]) done(i + c);
-                at += w[c];
-            }
-            return;
+            return at;
+        };
+        for (int it = warp; it < IT; it += kRegWarps) {
+            const u64 at = step_sum(it);
+            if (lane == 31) sh.step[it] = at;
+        }
+        __syncthreads();
+        if (warp != 0) return;
+        int it = 0;
+        while (it < IT - 1 && g >= run + sh.step[it]) run += sh.step[it++];
+        u64 at = run + step_sum(it);
+        for (int c = 3; c >= 0; --c) {
+            at -= own[c];
+            if (g >= at && g < at + own[c]) done(first + it * 128 + c);
         }
     };
 
@@ -963,7 +987,7 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
 
     const float u = a.uniform[row];
     const float least = fmaxf(cut, wt.floor);
-    pick(least, [&](float f, int i) { return f < least || (f == cut && i > last) ? 0ull : wt.final_whole(f); },
+    pick(least, [&](float f, int i) { return f < cut || (f == cut && i > last) ? 0ull : wt.final_whole(f); },
          [&](u64 total) { return goal_of(u, total); }, [&](int i) { a.token[row] = i; });
     cl.sync();    // nobody leaves while its memory may still be written
 }
