@@ -619,6 +619,7 @@ int mk_paged_attention_workspace(const mk_paged_kv *kv, int max_len, int n_q_hea
  *   n_tokens    rows of the buffers; rows of `out` from cu_seqlens[n_seqs] on
  *               are left as they were.
  *   max_len     host bound on the sequence lengths (sizes the launch).
+ *               (n_tokens / 128 + n_seqs) * n_q_heads is below 2^31.
  *   q, out      [n_tokens][n_q_heads][head_dim]; k, v [n_tokens][n_kv_heads]
  *               [head_dim]; all of `dtype`.  out must not overlap q, k or v.
  * Values of later tokens or other sequences never reach a row, whatever they

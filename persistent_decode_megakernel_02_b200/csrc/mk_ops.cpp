@@ -145,6 +145,8 @@ int mk_prompt_attention(int dtype, int n_q_heads, int n_kv_heads, int head_dim, 
     if (!heads_ok(n_q_heads, n_kv_heads, head_dim, dtype)) return MK_ERR_INVALID;
     if (!aligned(cu_seqlens, 4) || !aligned_or_null(status_out, 4)) return MK_ERR_INVALID;
     if (n_seqs < 1 || n_tokens < 0 || n_tokens > 0x7ffffc00 || max_len < 0) return MK_ERR_INVALID;
+    // the (row block, head) items fit an int
+    if (((double)n_tokens / 128 + n_seqs) * n_q_heads > 2147000000.0) return MK_ERR_INVALID;
     const long long qw = (long long)n_q_heads * head_dim, kw = (long long)n_kv_heads * head_dim;
     if (!rows_ok(q, q_stride, qw) || !rows_ok(out, out_stride, qw) || !rows_ok(k, k_stride, kw) ||
         !rows_ok(v, v_stride, kw))

@@ -29,6 +29,21 @@
 // shared memory and remembered per column with their first key; the epilogue
 // adds them to the rows that do see them.
 //
+// The code is kept small (loops over sequences, a tile's loads and the rare
+// paths are not unrolled): at 92 KB the SMs fetched most of every short item's
+// code from the instruction cache that a cluster of them shares, at 92 % of
+// its rate.  At 66 KB 1000 prompts of 20 tokens take 524 us instead of 559, 100
+// of 200 tokens 130 instead of 142; rolling the epilogue and the issuer's loop
+// over the units too (53 KB) gives 469 and 135, but costs long prompts 5 %.
+//
+// What bounds it: long prompts by the two softmax warps an SM sub-partition
+// has (1760 cycles for their two tiles of 128 weights a row, of which the
+// exponentials are 1024, against 1024 cycles of products at 128 dims): 8192
+// tokens of 32/8/128 heads 447 us, 1.23 PFLOP/s, 76 % of the matrix peak
+// measured in bursts.  With 64 dims the products are half of that and the
+// softmax is what remains: 6811 tokens in 9 prompts 72 us.  Short prompts by
+// the chain of one tile (load, S, softmax, P V, store).
+//
 // Tensor memory, 512 columns: S0 | S1 | O0 | O1, and for 64 dims P0 | P1: the
 // next tile's S is then computed while this one's softmax runs.  For 128 dims
 // P lies over the first half of its S.
@@ -71,7 +86,7 @@ struct PromptSmem {
 
 struct PromptItem {
     int row0, len;                 // the sequence's first row and length; len 0: no more items
-    int kvh, tiles;                // key tiles of the longer unit
+    int tiles;                     // key tiles of the longer unit
     int blk[2], head[2], n[2];     // per unit: row block, query head, key tiles (0: no such unit)
 };
 
@@ -110,6 +125,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
     }
 
     if (blockIdx.x == 0)
+#pragma unroll 1
         for (int i = tid; i < a.n_seqs; i += kPromptThreads) {
             const int b = a.cu[i], e = a.cu[i + 1];
             if (b < 0 || e < b || e > a.n_tokens || e - b > a.max_len) bad_value(a.status);
@@ -166,6 +182,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
     int low = 0;
     auto count = [&](int level) {
         int c = 0, shorter = 0;
+#pragma unroll 1
         for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
             const int levels = levels_of(s0 + lane);
             c += __popc(__ballot_sync(0xffffffffu, levels > level));
@@ -174,12 +191,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
         low = __reduce_max_sync(0xffffffffu, shorter);
         return c;
     };
-    int level = 0, here = 0;
+    int level = 0;
     if (warp == 8) {
         if (lane < 3) tma_prefetch_map(lane == 0 ? &p.q : lane == 1 ? &p.k : &p.v);
+#pragma unroll 1
         for (int s0 = 0; s0 < a.n_seqs; s0 += 32) level = max(level, levels_of(s0 + lane));
-        level = __reduce_max_sync(0xffffffffu, level) - 1;
-        here = level >= 0 ? count(level) : 0;
+        low = level = __reduce_max_sync(0xffffffffu, level);      // above the highest
     }
     tc_fence_before();
     __syncthreads();
@@ -189,78 +206,87 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
     if (warp >= 8) set_regs_down<kControlRegsPrompt>();
     if (warp == 8) {
         // ---- scheduler and loader
-        long long base = 0;                               // items before the level
-        int at = 0, passed = 0;      // the level's sequences before sequence `at`: the search goes on from there
-        const int P = gridDim.x;
+        uint32_t base = 0;           // items before the level
+        int here = 0;                // sequences that have it
+        int at = 0, passed = 0;      // those before sequence `at`: the search goes on from there
+        const uint32_t P = gridDim.x;
         int k = 0, F = 0;     // items published, tiles loaded
         bool ok = true;
-        for (long long turn = 0; ok; ++turn) {
-            const long long rank = turn * P + (turn & 1 ? P - 1 - blockIdx.x : blockIdx.x);
-            while (level >= 0 && rank >= base + (long long)here * per_seq) {
-                base += (long long)here * per_seq;
+        for (uint32_t turn = 0; ok; ++turn) {
+            const uint32_t rank = turn * P + (turn & 1 ? P - 1 - blockIdx.x : blockIdx.x);
+            while (level >= 0 && rank >= base + (uint32_t)here * per_seq) {
+                base += (uint32_t)here * per_seq;
                 --level;
                 at = passed = 0;
                 if (level < low) here = level >= 0 ? count(level) : 0;
             }
-            PromptItem it;
-            it.row0 = it.len = it.kvh = it.tiles = 0;
-            for (int u = 0; u < 2; ++u) it.blk[u] = it.head[u] = it.n[u] = 0;
+            // lanes 0 and 1 hold a unit each
+            int seq_row = 0, seq_len = 0, kvh = 0, head = 0, blk = 0, n = 0;
             if (level >= 0) {
-                const int nth = (int)((rank - base) / per_seq);
-                const int rem = (int)((rank - base) % per_seq);
-                it.kvh = rem % a.nkv;
+                const int nth = (int)((rank - base) / per_seq), rem = (int)(rank - base - (uint32_t)nth * per_seq);
+#pragma unroll 1
                 for (; at < a.n_seqs; at += 32) {
                     const unsigned m = __ballot_sync(0xffffffffu, levels_of(at + lane) > level);
-                    if (nth < passed + __popc(m)) {
-                        const int src = __fns(m, 0, nth - passed + 1);
-                        it.row0 = __shfl_sync(0xffffffffu, row0, src);
-                        it.len = __shfl_sync(0xffffffffu, len, src);
+                    const int ahead = nth - passed;
+                    if (ahead < __popc(m)) {
+                        const bool me = (m >> lane & 1u) && __popc(m & ((1u << lane) - 1)) == ahead;
+                        const int src = __ffs(__ballot_sync(0xffffffffu, me)) - 1;
+                        seq_row = __shfl_sync(0xffffffffu, row0, src);
+                        seq_len = __shfl_sync(0xffffffffu, len, src);
                         break;
                     }
                     passed += __popc(m);
                 }
-                const int blocks = (it.len + kTile - 1) / kTile;
-                for (int u = 0; u < 2; ++u) {
-                    const int unit = rem / a.nkv * 2 + u, blk = level * R + unit / G;
-                    if (blk >= blocks) break;
-                    it.blk[u] = blk;
-                    it.head[u] = it.kvh * G + unit % G;
-                    it.n[u] = blk + 1;
-                    it.tiles = blk + 1;
-                }
-                if (it.n[0] == 0) continue;      // a lone last row block has half the units
-                if (it.n[1] == 0) it.blk[1] = it.blk[0];
+                const int pair = rem / a.nkv, unit = pair * 2 + (lane & 1), row_blk = unit / G;
+                kvh = rem - pair * a.nkv;
+                head = kvh * G + unit - row_blk * G;
+                blk = level * R + row_blk;
+                if (blk < (seq_len + kTile - 1) / kTile) n = blk + 1;
             }
+            const int n0 = __shfl_sync(0xffffffffu, n, 0), n1 = __shfl_sync(0xffffffffu, n, 1), tiles = max(n0, n1);
+            if (level >= 0 && n0 == 0) continue;      // a lone last row block has half the units
             const int slot = k & 1;
             if (k >= 2) ok = mbar_wait_warp(&t.item_empty[slot], ((k >> 1) - 1) & 1, &t.abort);
             if (!ok) break;
-            if (lane == 0) {
-                t.item[slot] = it;
-                mbar_arrive(&t.item_full[slot]);
+            PromptItem &it = t.item[slot];
+            const int blk0 = __shfl_sync(0xffffffffu, blk, 0);
+            if (lane < 2) {
+                it.head[lane] = head;
+                it.blk[lane] = n ? blk : blk0;
+                it.n[lane] = n;
             }
+            if (lane == 0) {
+                it.row0 = seq_row;
+                it.len = seq_len;
+                it.tiles = tiles;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&t.item_full[slot]);
             if (level < 0) break;
             if (k > 0) ok = mbar_wait_warp(&t.q_empty, (k - 1) & 1, &t.abort);
             if (!ok) break;
             ++k;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&t.q_full, (it.n[1] ? 2 : 1) * L::kTileBytes);
+            const int units = n1 ? 2 : 1;
+            if (lane == 0) mbar_arrive_expect_tx(&t.q_full, units * L::kTileBytes);
+            __syncwarp();
+            if (lane < units)
                 for (int h = 0; h < D / 64; ++h)
-                    for (int u = 0; u < (it.n[1] ? 2 : 1); ++u)
-                        tma_load_3d(smem + L::kQ + u * L::kTileBytes + h * kTile * 128, &p.q, h * 64, it.head[u],
-                                    it.row0 + it.blk[u] * kTile, &t.q_full);
-            }
-            for (int f = 0; f < 2 * it.tiles && ok; ++f, ++F) {       // K0 V0 K1 V1 ...
+                    tma_load_3d(smem + L::kQ + lane * L::kTileBytes + h * kTile * 128, &p.q, h * 64, head, seq_row + blk * kTile,
+                                &t.q_full);
+#pragma unroll 1
+            for (int f = 0; f < 2 * tiles && ok; ++f, ++F) {       // K0 V0 K1 V1 ...
                 const int st = F % L::kStages, use = F / L::kStages;
                 if (use > 0) ok = mbar_wait_warp(&t.empty[st], (use - 1) & 1, &t.abort);
                 if (ok && lane == 0) {
                     mbar_arrive_expect_tx(&t.full[st], L::kTileBytes);
                     for (int h = 0; h < D / 64; ++h)
                         tma_load_3d(smem + L::kRing + st * L::kTileBytes + h * kTile * 128, f & 1 ? &p.v : &p.k, h * 64,
-                                    it.kvh, it.row0 + (f >> 1) * kTile, &t.full[st]);
+                                    kvh, seq_row + (f >> 1) * kTile, &t.full[st]);
                 }
             }
         }
         // every tile used: nothing is in flight when the block ends
+#pragma unroll 1
         for (int st = 0; st < L::kStages && ok; ++st) {
             const int uses = (F - st + L::kStages - 1) / L::kStages;
             if (uses > 0) ok = mbar_wait_warp(&t.empty[st], (uses - 1) & 1, &t.abort);
@@ -320,8 +346,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                 for (int u = 0; u < 2; ++u) {
                     if (j >= (u ? n1 : n0) || !ok) continue;
                     if (kOwnP) {
-                        if (products[u] > 0) ok = mbar_wait_warp(&t.s_free[u], (products[u] - 1) & 1, &t.abort);
-                        ++products[u];
+                        // (of a fresh barrier the phase before the first counts as over)
+                        ok = mbar_wait_warp(&t.s_free[u], (products[u]++ & 1) ^ 1, &t.abort);
                         tc_fence_after();
                     }
                     if (ok) ok = full(F + 2 * j);
@@ -350,7 +376,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                     const int n = u ? n1 : n0;
                     if (j >= n || !ok) continue;
                     ok = mbar_wait_warp(&t.p_ready[u], tiles[u]++ & 1, &t.abort);
-                    if (ok && j == 0 && outs[u] > 0) ok = mbar_wait_warp(&t.o_empty[u], (outs[u] - 1) & 1, &t.abort);
+                    if (ok && j == 0) ok = mbar_wait_warp(&t.o_empty[u], (outs[u] & 1) ^ 1, &t.abort);
                     if (ok && mask)
                         ok = mbar_wait_warp(&t.guard_done[j - blk0], (j == blk0 ? masked[0] : masked[1]) & 1, &t.abort);
                     if (!ok) continue;
@@ -397,14 +423,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                 uint4 *tile = reinterpret_cast<uint4 *>(smem + L::kRing + f % L::kStages * L::kTileBytes);
                 constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u, kOne = kBf16 ? 0x00800080u : 0x04000400u;
                 uint32_t bad = 0;
-#pragma unroll 8
+#pragma unroll 4
                 for (int i = gt; i < L::kTileBytes / 16; i += 64) {
                     const uint4 x = tile[i];
                     bad |= ((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne);
                 }
                 if (bad & 0x80008000u) {
                     uint16_t *e = reinterpret_cast<uint16_t *>(tile);
+#pragma unroll 1
                     for (int i = gt; i < L::kTileBytes / 16; i += 64)
+#pragma unroll 1
                         for (int c = 0; c < 8; ++c) {
                             const uint32_t w = e[i * 8 + c];
                             if ((w & kExp & 0xffffu) != (kExp & 0xffffu)) continue;
@@ -561,16 +589,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&t.o_empty[u]);
                     }
-                    if (any)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int col = q * 32 + i;
-                            float o = __uint_as_float(x[i]);
-                            if (t.first[slot][0][col] <= pos) o = NAN;
-                            if (t.first[slot][1][col] <= pos) o += INFINITY;
-                            if (t.first[slot][2][col] <= pos) o -= INFINITY;
-                            x[i] = __float_as_uint(o);
-                        }
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
                         uint4 w;
@@ -580,6 +598,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                         w.w = T::pack(__uint_as_float(x[i + 6]) * inv, __uint_as_float(x[i + 7]) * inv);
                         *staged(lane, i / 8) = w;
                     }
+                    if (any)
+#pragma unroll 1
+                        for (int i = 0; i < 32; ++i) {
+                            const int col = q * 32 + i;
+                            uint16_t *e = reinterpret_cast<uint16_t *>(staged(lane, i / 8)) + i % 8;
+                            float o = T::unpack(*e).x;
+                            if (t.first[slot][0][col] <= pos) o = NAN;
+                            if (t.first[slot][1][col] <= pos) o += INFINITY;
+                            if (t.first[slot][2][col] <= pos) o -= INFINITY;
+                            *e = (uint16_t)T::pack(o, 0.f);
+                        }
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {

@@ -85,7 +85,7 @@ def test_paged_refusals(bad):
 
 @pytest.mark.parametrize("bad", [
     dict(dtype=2), dict(nq=5), dict(nq=0), dict(nkv=0), dict(nq=18), dict(d=80), dict(d=256), dict(cu=None),
-    dict(cu=A + 2), dict(ns=0), dict(n=-1), dict(n=(1 << 31) - 1), dict(max_len=-1), dict(q=None), dict(qs=255), dict(qs=0), dict(k=A + 2),
+    dict(cu=A + 2), dict(ns=0), dict(n=-1), dict(n=(1 << 31) - 1), dict(ns=1 << 29, nq=8, nkv=4, n=1, qs=512, os=512, ks=256, vs=256), dict(max_len=-1), dict(q=None), dict(qs=255), dict(qs=0), dict(k=A + 2),
     dict(ks=64), dict(v=None), dict(vs=129), dict(scale=0.0), dict(scale=math.nan), dict(out=None), dict(os=192),
     dict(status=A + 3)], ids=str)
 def test_prompt_refusals(bad):
