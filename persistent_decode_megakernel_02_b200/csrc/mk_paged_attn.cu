@@ -23,9 +23,8 @@
 // tensor rate either way.
 //
 // The softmax weights enter the value product as a 16-bit value and the
-// 16-bit remainder, so the output keeps the accuracy of 32-bit weights: with
-// up to 4 heads per KV head the remainders ride in the unused columns 4-7
-// (queries duplicated there), above that in a second product.
+// 16-bit remainder, in two products, so the output keeps the accuracy of
+// 32-bit weights.
 #include "mk_ops.cuh"
 
 namespace mk {
@@ -90,7 +89,7 @@ struct PagedParams {
     int max_blocks;      // counters in the workspace
 };
 
-template <class T, int D, bool G4>
+template <class T, int D>
 __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(const __grid_constant__ PagedParams p) {
     using S = PagedShape<D>;
     constexpr int NW = S::kWarps, NT = S::kThreads, KG = S::kGran, JK = D / 32, JV = D / 64;
@@ -108,11 +107,10 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
     auto clamped = [&](int n) { return min(max(n, 0), a.max_len); };
     auto steps_of = [&](int n) { return (n + S::kStep - 1) / S::kStep; };
 
-    // ---- this block's part of the work.  Two rules, by what the lengths give:
-    //  one item per block (`single`): an item is cut into equal parts of at
-    //   most C steps, C such that all parts fit the grid;
-    //  ranges: all items end to end, each with `item_cost` steps ahead of its
-    //   own for what it costs whatever its length, cut into equal ranges.
+    // ---- this block's part of the work: all items end to end, each with
+    // kItemCost steps ahead of its own, cut into equal ranges.  (A second rule
+    // for few items, equal parts of one item a block, was slower by 0.4 us at
+    // one sequence of 551 and of 16385 positions and at 16 of up to 2048.)
     const int n0 = lane < ns ? a.lens[lane] : 0;
     auto len_of = [&](int s0) { return s0 == 0 ? clamped(n0) : s0 + lane < ns ? clamped(a.lens[s0 + lane]) : 0; };
     int total = 0, items = 0;
@@ -127,20 +125,11 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
     }
     const int all_items = items * nkv;
     total *= nkv;
-    const bool single = 2 * all_items <= P;
-    int per, lo, hi;
-    if (single) {
-        per = max((total + P - all_items - 1) / (P - all_items), S::kMinSteps);
-        lo = blk;
-        hi = P;
-    } else {
-        total += all_items * kItemCost;
-        per = max((total - 1) / P + 1, S::kMinSteps);
-        lo = min(blk * per, total);   // blk * per < total + P * kMinSteps
-        hi = min(total, lo + per);
-    }
-    auto parts_of = [&](int n) { return (steps_of(n) + per - 1) / per; };   // single
-    auto cost_of = [&](int n) { return n <= 0 ? 0 : single ? parts_of(n) : steps_of(n) + kItemCost; };
+    total += all_items * kItemCost;
+    const int per = max((total - 1) / P + 1, S::kMinSteps);
+    const int lo = min(blk * per, total);   // blk * per < total + P * kMinSteps
+    const int hi = min(total, lo + per);
+    auto cost_of = [&](int n) { return n <= 0 ? 0 : steps_of(n) + kItemCost; };
 
     // empty sequences get zeros; lengths outside the bounds are reported
     auto empties = [&] {
@@ -183,33 +172,21 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
     while (true) {
         const int steps = steps_of(len), cost = cost_of(len);
         const int h = (cur - seq0) / cost;
-        int b, e, first, parts;   // steps [b, e) of the item; its parts are blocks first..
-        if (single) {
-            const int i = cur - seq0 - h * cost;
-            parts = cost;
-            first = blk - i;
-            b = (int)((long long)steps * i / parts);
-            e = (int)((long long)steps * (i + 1) / parts);
-            cur = hi;
-        } else {
-            const int item0 = seq0 + h * cost + kItemCost;   // its first step
-            b = max(cur - item0, 0);
-            e = min(hi, item0 + steps) - item0;
-            first = item0 / per;
-            parts = (item0 + steps - 1) / per - first + 1;
-            cur = item0 + steps;
-        }
+        // steps [b, e) of the item; its parts are blocks first..
+        const int item0 = seq0 + h * cost + kItemCost;   // its first step
+        const int b = max(cur - item0, 0), e = min(hi, item0 + steps) - item0;
+        const int first = item0 / per, parts = (item0 + steps - 1) / per - first + 1;
+        cur = item0 + steps;
         if (e > b) {
 
-        // queries of this KV head: lane (g, t) holds head g's (G4: head g % 4's)
-        // elements [(4 j + t) 8, +8)
+        // queries of this KV head: lane (g, t) holds head g's elements
+        // [(4 j + t) 8, +8)
         uint4 q[JK];
         {
-            const int hq = G4 ? g & 3 : g;
-            const uint16_t *src = (const uint16_t *)a.q + seq * a.q_stride + (long long)(h * G + hq) * D + t * 8;
+            const uint16_t *src = (const uint16_t *)a.q + seq * a.q_stride + (long long)(h * G + g) * D + t * 8;
 #pragma unroll
             for (int j = 0; j < JK; ++j)
-                q[j] = hq < G ? *reinterpret_cast<const uint4 *>(src + j * 32) : make_uint4(0, 0, 0, 0);
+                q[j] = g < G ? *reinterpret_cast<const uint4 *>(src + j * 32) : make_uint4(0, 0, 0, 0);
         }
         float acc[JV * 4][4];
 #pragma unroll
@@ -319,11 +296,8 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
                     const uint32_t wh = T::pack(w0, w1);
                     const float2 back = T::unpack(wh);
                     const uint32_t wl = T::pack(w0 - back.x, w1 - back.y);
-                    if constexpr (G4) hi2[x] = transpose8(t < 2 ? wh : wl);
-                    else {
-                        hi2[x] = transpose8(wh);
-                        lo2[x] = transpose8(wl);
-                    }
+                    hi2[x] = transpose8(wh);
+                    lo2[x] = transpose8(wl);
                 }
 #pragma unroll
                 for (int j = 0; j < JV; ++j)
@@ -334,7 +308,7 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
                         const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632),
                                        a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
                         mma16816<T>(acc[j * 4 + y], a0, a1, a2, a3, hi2[0], hi2[1]);
-                        if constexpr (!G4) mma16816<T>(acc[j * 4 + y], a0, a1, a2, a3, lo2[0], lo2[1]);
+                        mma16816<T>(acc[j * 4 + y], a0, a1, a2, a3, lo2[0], lo2[1]);
                     }
             }
             load_v(next);
@@ -346,26 +320,18 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             for (int o = 4; o < 32; o <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
-        if constexpr (G4) {
 #pragma unroll
-            for (int y = 0; y < JV * 4; ++y)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) acc[y][k] += __shfl_xor_sync(0xffffffffu, acc[y][k], 2);
-        }
-        if (!G4 || t < 2) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if (g == 0) {
-                    sm[warp][2 * t + k] = m[k];
-                    sl[warp][2 * t + k] = l[k];
-                }
-#pragma unroll
-                for (int j = 0; j < JV; ++j)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        *reinterpret_cast<float2 *>(&so[warp][2 * t + k][(j * 8 + g) * 8 + 2 * y]) =
-                            make_float2(acc[j * 4 + y][k], acc[j * 4 + y][2 + k]);
+        for (int k = 0; k < 2; ++k) {
+            if (g == 0) {
+                sm[warp][2 * t + k] = m[k];
+                sl[warp][2 * t + k] = l[k];
             }
+#pragma unroll
+            for (int j = 0; j < JV; ++j)
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    *reinterpret_cast<float2 *>(&so[warp][2 * t + k][(j * 8 + g) * 8 + 2 * y]) =
+                        make_float2(acc[j * 4 + y][k], acc[j * 4 + y][2 + k]);
         }
         __syncthreads();
         const bool whole = b == 0 && e == steps;
@@ -487,10 +453,7 @@ size_t paged_workspace(const mk_paged_kv &kv, int max_len, int, int num_sms) {
 
 template <class T, int D>
 static void paged_go(const PagedParams &p, int grid, cudaStream_t stream) {
-    if (p.a.n_q_heads / p.a.kv.n_kv_heads <= 4)
-        paged_attn_kernel<T, D, true><<<grid, PagedShape<D>::kThreads, 0, stream>>>(p);
-    else
-        paged_attn_kernel<T, D, false><<<grid, PagedShape<D>::kThreads, 0, stream>>>(p);
+    paged_attn_kernel<T, D><<<grid, PagedShape<D>::kThreads, 0, stream>>>(p);
 }
 
 cudaError_t paged_launch(const PagedArgs &a, int, int num_sms, cudaStream_t stream) {

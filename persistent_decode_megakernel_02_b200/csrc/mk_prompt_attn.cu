@@ -22,8 +22,8 @@
 // rare.  l, the row's sum, stays in 32 bits in its thread; out = O / l.
 //
 // Roles: warps 0-3 and 4-7 the softmax of unit 0 and 1 (warp w reads tensor
-// memory lanes 32 (w % 4)..), warp 8 a TMA loader (one thread), warp 9 the
-// MMA issuer (one thread), warps 10-11 the guard of the masked tiles: a zero
+// memory lanes 32 (w % 4)..), warp 8 the scheduler and TMA loader, warp 9 the
+// MMA issuer, warps 10-11 the guard of the masked tiles: a zero
 // weight times a NaN or an infinity is not zero, so in the tiles that hold
 // keys some row must not see, values that are not finite are taken out of
 // shared memory and remembered per column with their first key; the epilogue
@@ -36,13 +36,13 @@
 // of 200 tokens 130 instead of 142; rolling the epilogue and the issuer's loop
 // over the units too (53 KB) gives 469 and 135, but costs long prompts 5 %.
 //
-// What bounds it: long prompts by the two softmax warps an SM sub-partition
-// has (1760 cycles for their two tiles of 128 weights a row, of which the
-// exponentials are 1024, against 1024 cycles of products at 128 dims): 8192
-// tokens of 32/8/128 heads 447 us, 1.23 PFLOP/s, 76 % of the matrix peak
-// measured in bursts.  With 64 dims the products are half of that and the
-// softmax is what remains: 6811 tokens in 9 prompts 72 us.  Short prompts by
-// the chain of one tile (load, S, softmax, P V, store).
+// What bounds it: a unit's tile is a chain (products, softmax, products; 1024
+// cycles of matrix work at 128 dims, and 1320 of a softmax warp alone, 1760
+// beside the other unit's), of which the two units overlap two: 8192 tokens
+// of 32/8/128 heads 447 us, 1.23 PFLOP/s, 76 % of the matrix peak measured in
+// bursts.  With 64 dims the products are half of that and the softmax is what
+// remains: 6811 tokens in 9 prompts 72 us.  Short prompts by the latency of
+// one tile's chain from load to store.
 //
 // Tensor memory, 512 columns: S0 | S1 | O0 | O1, and for 64 dims P0 | P1: the
 // next tile's S is then computed while this one's softmax runs.  For 128 dims

@@ -22,6 +22,12 @@
 //    bits left).
 //
 // Rows beyond 8 blocks' shared memory take one block each that rereads them.
+//
+// What bounds it: one row, the latency of its exchanges between blocks (2.3 us
+// of load, then about 1 us an exchange): 9.4 us at 128256 logits with every
+// filter, 26.6 with top-p alone; many rows, the 64-bit weights (12 cycles an SM
+// for 32 of them) and the histogram's atomics of the rows that need them all:
+// 64 mixed ones 43 us, 256 with top-k 101 us (1.3 TB/s), with top-p 300.
 #include <atomic>
 #include <utility>
 
@@ -326,9 +332,13 @@ namespace cg = cooperative_groups;
 
 constexpr int kRegThreads = 512, kRegWarps = kRegThreads / 32, kMaxCluster = 8;
 constexpr int kListMax = 512;                  // gathered logits, at most
-constexpr int kMaxK = 384;                     // top-k by the threads' maxima, at most
+// top-k by the threads' maxima, at most (one row of 128256, against the exact
+// cut: k = 50 10.3 and 32.3 us, 200 14.8 and 32.5, 384 24.6 and 32.8; 64 rows of
+// 32000: 10.8 and 32.8, 19.5 and 33.4, 39.5 and 33.8)
+constexpr int kMaxK = 384;
 constexpr int kVecStep = 4 * kRegThreads;      // logits of one vector step of a block
 constexpr int kMaxIt = 22;                     // vector steps of a slice: 176 KB of logits
+constexpr int kStepsForTwo = 10;               // with which two blocks fit an SM
 
 struct RegShared {
     union {
@@ -364,6 +374,9 @@ struct RegShared {
     uint32_t tmp32[kRegWarps];
     u64 goal;
 };
+
+static_assert(sizeof(RegShared) + kMaxIt * kVecStep * 4 <= 227 * 1024, "a slice fits a block's shared memory");
+static_assert(2 * (sizeof(RegShared) + kStepsForTwo * kVecStep * 4 + 1024) <= 228 * 1024, "two blocks an SM");
 
 template <class V>
 __device__ __forceinline__ V block_max(V v, V *tmp) {
@@ -995,12 +1008,17 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
 }  // namespace
 
 cudaError_t sample_launch(const SampleArgs &a, int device, int num_sms, cudaStream_t stream) {
-    // Eight blocks a row from 8 vector steps each on; shorter rows take fewer.
-    // (up to 3 logits ahead of a row that starts inside a 16-byte word)
+    // Up to eight blocks a row, as many as get a vector step each; fewer where
+    // that brings all rows onto the device at once and two blocks still fit an
+    // SM (64 rows of 32000, 8 and 4 blocks a row: top-k 20.1 and 10.8 us, top-p
+    // 44 and 28; one row: 8.2 and 8.7, 17 and 20).  (Up to 3 logits lie ahead of
+    // a row that starts inside a 16-byte word.)
     const int need = a.vocab + 3;
+    auto steps_of = [&](int blocks) { return (need + blocks * kVecStep - 1) / (blocks * kVecStep); };
     int cluster = 1;
-    while (cluster < kMaxCluster && need > cluster * kVecStep) cluster *= 2;
-    const int steps = (need + cluster * kVecStep - 1) / (cluster * kVecStep);
+    while (cluster < kMaxCluster && steps_of(cluster) > 1) cluster *= 2;
+    while (cluster > 1 && (long long)a.rows * cluster > 2 * num_sms && steps_of(cluster / 2) <= kStepsForTwo) cluster /= 2;
+    const int steps = steps_of(cluster);
     if (steps > kMaxIt) {
         sample_long_kernel<<<a.rows, kSampThreads, 0, stream>>>(a);
         return cudaGetLastError();
