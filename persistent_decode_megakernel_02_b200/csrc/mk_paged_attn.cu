@@ -25,6 +25,12 @@
 // The softmax weights enter the value product as a 16-bit value and the
 // 16-bit remainder, in two products, so the output keeps the accuracy of
 // 32-bit weights.
+//
+// What bounds it: 203000 positions in 32 sequences of 8 x 128 take 129 us,
+// 6.45 TB/s, 98 % of the copy rate.  At 34 MB (16 sequences of up to 2048, one
+// of 16385: 13.7 and 12.6 us, 5.2 by the copy rate) the chain of dependent
+// latencies around the stream does: lengths, page table, first rows, and the
+// merge through the workspace; one sequence of 551 is that chain alone, 6.7 us.
 #include "mk_ops.cuh"
 
 namespace mk {
@@ -33,7 +39,8 @@ namespace {
 constexpr int kMaxBlocksPerSm = 2;
 // An item costs a block about this many steps whatever its length (one
 // 128-position item a block: 4.7 us in all, 17 items of 2 steps one after
-// another 30 us).
+// another 30 us).  4 / 8 / 16 / 24: 64 ragged sequences of up to 1000 33, 25, 24,
+// 25 us, 16 of up to 2048 15.2, 15.0, 13.6, 14.6.
 constexpr int kItemCost = 16;
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t *p) {
@@ -71,10 +78,10 @@ template <int D>
 struct PagedShape {
     static constexpr int kGran = D == 64 ? 2 : 1;    // 16-key groups per step
     static constexpr int kStep = 16 * kGran;         // keys per step: 8 KB of K and V
-    // least part of an item (4096 positions of 8 KV heads, 4 / 8 / 16 / 24 / 32
-    // steps: 9.3, 9.3, 9.4, 10.5, 11.8 us for 64 dims, 12.6, 12.6, 10.2, 12.0,
-    // 12.7 for 128)
-    static constexpr int kMinSteps = D == 64 ? 8 : 16;
+    // least part of an item (one sequence of 551 and one of 4096 positions, 8 KV
+    // heads: 64 dims 4 steps 6.7 and 9.9 us, 8 7.6 and 9.2, 16 8.4 and 10.3; 128
+    // dims 8 steps 9.1 and 13.2, 16 9.7 and 11.2, 24 12.9 and 12.8)
+    static constexpr int kMinSteps = D == 64 ? 4 : 16;
     static constexpr int kWarps = D == 64 ? 8 : 6;
     static constexpr int kThreads = kWarps * 32;
 };
