@@ -850,6 +850,49 @@ assert d <= 3 * 2.0 ** -8 * v.float().abs().max(), d
     assert r.returncode == 0, r.stderr[-2000:]
 
 
+def test_offsets_beyond_32_bits(mk):
+    """Rows and pages more than 2^32 elements from their buffers' starts."""
+    n, nq, nkv, d, ps = 300, 4, 2, 64, 16
+    g = gen(26)
+    stride = 1 << 24
+    buf = torch.empty(n * stride, device="cuda", dtype=torch.bfloat16)
+    rows = lambda heads, at: buf.as_strided((n, heads, d), (stride, d, 1), at)
+    q, k, v, out = rows(nq, 0), rows(nkv, 4096), rows(nkv, 8192), rows(nq, 12288)
+    for x in (q, k, v):
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+    q0, k0, v0 = q.clone(), k.clone(), v.clone()
+    per = 20
+    pages = (1 << 32) // (nkv * ps * d) + per + 3
+    kc = torch.empty(pages, nkv, ps, d, device="cuda", dtype=torch.bfloat16)
+    table = torch.arange(pages - 1, pages - 1 - per, -1, device="cuda", dtype=torch.int32)[None].contiguous()
+    table[0, 3] = 5
+    cache = mk.PagedKV(kc, torch.empty_like(kc), table)
+    status = ints([0])
+    mk.kv_append(cache, q, k, v, ints([0, n]), ints([0]), 1e4, status=status)
+    pos = torch.arange(n, device="cuda", dtype=torch.float64)
+    e = torch.finfo(torch.bfloat16).eps
+    ref, r = rotate64(q0, pos, 1e4)
+    assert ((q.double() - ref).abs() <= e / 2 * ref.abs() + 2.0 ** -21 * r + 1e-7).all()
+    ref, r = rotate64(k0, pos, 1e4)
+    for p in range(n):
+        got = kc[table[0, p // ps], :, p % ps]
+        assert ((got.double() - ref[p]).abs() <= e / 2 * ref[p].abs() + 2.0 ** -21 * r[p] + 1e-7).all()
+        assert torch.equal(cache.v[table[0, p // ps], :, p % ps], v0[p])
+    mk.prompt_attention(q, k, v, ints([0, n]), n, out, status=status)
+    prompt_check(q.contiguous(), k.contiguous(), v.contiguous(), [n], out.contiguous(), d ** -0.5)
+    mk.paged_attention(cache, q[n - 1:], ints([n]), n, out[n - 1:], status=status)
+    paged_check(cache, q[n - 1:].clone(), [n], out[n - 1:].clone(), d ** -0.5)
+    assert int(status) == 0
+    del buf, q, k, v, out, kc, cache
+    torch.cuda.empty_cache()
+    stride = 1 << 28
+    x = torch.empty(18 * stride, device="cuda").as_strided((18, 40000), (stride, 1))
+    x.copy_(noise(18, 40000, 27))
+    sample_case(mk, x, k=[40] * 9 + [0] * 9, p=[0.9] * 18)
+    del x
+    torch.cuda.empty_cache()
+
+
 def test_calls_at_once_on_two_streams(mk):
     # everything twice, on two streams at the same time, each with its own buffers
     g = gen(22)
