@@ -812,10 +812,11 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
         }
         __syncthreads();
         const uint32_t in_group = sh.found_bin;
+        const u64 before_group = sh.found_mass;      // read before the scan: it is written again after it
         if (in_group != 0xffffffffu) {
             const u64 mass = over_blocks([&](const RegShared *o) { return tid < 256 ? o->sums[in_group * 32 + (tid >> 3)] : 0; });
             u64 sum;
-            const u64 at = sh.found_mass + reg_block_scan(tid & 7 ? 0 : mass, sh.tmp64, sum);      // synchronises
+            const u64 at = before_group + reg_block_scan(tid & 7 ? 0 : mass, sh.tmp64, sum);      // synchronises
             if (tid < 256 && (tid & 7) == 0 && !reached(at) && reached(at + mass)) {
                 sh.found_bin = in_group * 32 + (tid >> 3);
                 sh.found_mass = at;
