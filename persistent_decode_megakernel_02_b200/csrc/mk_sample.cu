@@ -24,10 +24,10 @@
 // Rows beyond 8 blocks' shared memory take one block each that rereads them.
 //
 // What bounds it: one row, the latency of its exchanges between blocks (2.3 us
-// of load, then about 1 us an exchange): 9.4 us at 128256 logits with every
+// of load, then about 1 us an exchange): 9.3 us at 128256 logits with every
 // filter, 26.6 with top-p alone; many rows, the 64-bit weights (12 cycles an SM
 // for 32 of them) and the histogram's atomics of the rows that need them all:
-// 64 mixed ones 43 us, 256 with top-k 101 us (1.3 TB/s), with top-p 300.
+// 64 mixed ones 42 us, 256 with top-k 101 us (1.3 TB/s), with top-p 300.
 #include <atomic>
 #include <utility>
 
@@ -871,13 +871,43 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
     // done(index).  Logits below `least` weigh nothing.
     auto pick = [&](float least, auto weight, auto goal, auto done) {
         u64 s = 0;
+        if (least > wt.reach) {
+            // a part of the row: of 32 logits a thread those that are in it, two at a
+            // time (64 mixed rows 42.8 -> 41.7 us against all four of a vector with one)
+#pragma unroll 1
+            for (int it0 = 0; it0 < IT; it0 += 8) {
+                uint32_t in = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (it0 + j < IT) {
+                        const float4 q = xs[(it0 + j) * kRegThreads + tid];
+                        in |= ((q.x >= least ? 1u : 0u) | (q.y >= least ? 2u : 0u) | (q.z >= least ? 4u : 0u) | (q.w >= least ? 8u : 0u))
+                              << 4 * j;
+                    }
+                while (in) {
+                    int i[2];
+                    float f[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int b = __ffs(in) - 1, it = it0 + (b >> 2);
+                        f[j] = -INFINITY;
+                        i[j] = 0;
+                        if (b >= 0) {
+                            f[j] = reinterpret_cast<const float *>(xs)[(it * kRegThreads + tid) * 4 + (b & 3)];
+                            i[j] = base + it * 128 + (b & 3);
+                        }
+                        in &= in - 1;
+                    }
+                    s += weight(f[0], i[0]) + weight(f[1], i[1]);
+                }
+            }
+        } else
 #pragma unroll 2
-        for (int it = 0; it < IT; ++it) {
-            const float4 q = xs[it * kRegThreads + tid];
-            const int i = base + it * 128;
-            if (fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)) >= least)
+            for (int it = 0; it < IT; ++it) {
+                const float4 q = xs[it * kRegThreads + tid];
+                const int i = base + it * 128;
                 s += weight(q.x, i) + weight(q.y, i + 1) + weight(q.z, i + 2) + weight(q.w, i + 3);
-        }
+            }
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         __syncthreads();
         if (lane == 0) sh.sub[warp] = s;
