@@ -482,7 +482,7 @@ __device__ __forceinline__ int row_in_order(const SampleArgs &a, int c) {
     return row0 + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
 }
 
-// A block's slice of the row is 16 warps\' parts of IT vector steps (4 logits a
+// A block's slice of the row is 16 warps' parts of IT vector steps (4 logits a
 // lane), so index order is (warp, step, lane, element).  A thread only ever
 // reads the logits it stored; NaN is stored as -infinity.
 __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, int IT, bool in_order) {
