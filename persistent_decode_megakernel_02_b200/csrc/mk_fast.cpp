@@ -28,19 +28,26 @@ struct Rows {
     long long stride = 0;
 };
 
+// Stride between the tokens of a [rows][heads][d] tensor whose heads are
+// contiguous, -1 for any other layout.  Of a single row the row stride does not
+// matter, its heads' and elements' do; of no rows nothing does.  The binding's
+// other way asks this function too.
+int64_t row_stride_of(const at::Tensor &t) {
+    if (t.dim() != 3) return -1;
+    const int64_t n = t.size(0), heads = t.size(1), d = t.size(2);
+    if (n > 0 && ((d > 1 && t.stride(2) != 1) || (heads > 1 && t.stride(1) != d))) return -1;
+    return n > 1 ? t.stride(0) : heads * d;
+}
+
 // A [rows][heads][d] tensor whose heads are contiguous.
 bool rows(PyObject *o, at::ScalarType dt, int dev, int64_t n, int64_t heads, int64_t d, Rows &r) {
     const at::Tensor *t = tensor(o);
     if (!t || t->scalar_type() != dt || !t->is_cuda() || t->get_device() != dev || t->dim() != 3 || t->size(0) != n ||
         t->size(1) != heads || t->size(2) != d)
         return false;
-    if (n > 1) {
-        if (t->stride(2) != 1 || (heads > 1 && t->stride(1) != d)) return false;
-        r.stride = t->stride(0);
-    } else
-        r.stride = heads * d;
+    r.stride = row_stride_of(*t);
     r.p = t->data_ptr();
-    return true;
+    return r.stride >= 0;
 }
 
 // A contiguous vector of n; None gives a null pointer where `optional`.
@@ -186,7 +193,19 @@ PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     });
 }
 
+// row_stride(tensor): row_stride_of
+PyObject *row_stride(PyObject *, PyObject *o) {
+    const at::Tensor *t = tensor(o);
+    int64_t stride = -1;
+    try {
+        if (t) stride = row_stride_of(*t);
+    } catch (...) {      // a tensor without strides
+    }
+    return PyLong_FromLongLong(stride);
+}
+
 PyMethodDef methods[] = {
+    {"row_stride", row_stride, METH_O, nullptr},
     {"kv_append", (PyCFunction)(void *)kv_append, METH_FASTCALL, nullptr},
     {"paged_attention", (PyCFunction)(void *)paged_attention, METH_FASTCALL, nullptr},
     {"prompt_attention", (PyCFunction)(void *)prompt_attention, METH_FASTCALL, nullptr},

@@ -41,6 +41,7 @@ if not os.path.exists(LIB_PATH):
 _lib = C.CDLL(LIB_PATH)
 import torch  # noqa: E402  (before _mk_fast, which links against it)
 from . import _mk_fast as _fast  # noqa: E402
+from ._mk_fast import row_stride as _row_stride  # noqa: E402
 
 
 class MkError(RuntimeError):
@@ -418,13 +419,10 @@ def _rows(what: str, name: str, t, dtype, dev: int, shape: tuple) -> int:
     contiguous."""
     if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
         _invalid(what, f"{name} must be {dtype} {list(shape)} on cuda:{dev}, got {t.dtype} {list(t.shape)} on {t.device}")
-    st = t.stride()
-    rows, heads, d = shape
-    if rows <= 1:
-        return heads * d
-    if st[2] != 1 or (st[1] != d and heads > 1):
+    stride = _row_stride(t)
+    if stride < 0:
         _invalid(what, f"{name}'s heads must be contiguous")
-    return st[0]
+    return stride
 
 
 def _vec(what: str, name: str, t, dtype, dev: int, n: int):

@@ -163,3 +163,33 @@ def test_binding_checks_its_tensors():
         mk.sample(torch.zeros(1, 8), torch.zeros(1), torch.zeros(1, dtype=torch.int32))
     with pytest.raises(mk.MkError):
         mk.prompt_attention(k[0], k[0], k[0], torch.zeros(2, dtype=torch.int32), 4, k[0])
+
+
+def one_row_layouts():
+    """[1][8][64] views whose heads are not contiguous."""
+    import torch
+    x = torch.zeros(1, 8, 3, 64, dtype=torch.bfloat16)
+    return {"interleaved": x[:, :, 1], "transposed": torch.zeros(1, 64, 8, dtype=torch.bfloat16).transpose(1, 2),
+            "sliced": torch.zeros(1, 8, 128, dtype=torch.bfloat16)[..., :64],
+            "every second": torch.zeros(1, 8, 128, dtype=torch.bfloat16)[..., ::2],
+            "expanded heads": torch.zeros(1, 1, 64, dtype=torch.bfloat16).expand(1, 8, 64),
+            "expanded elements": torch.zeros(1, 8, 1, dtype=torch.bfloat16).expand(1, 8, 64)}
+
+
+@pytest.mark.parametrize("name", list(one_row_layouts()))
+def test_a_single_row_has_contiguous_heads_too(name):
+    t = one_row_layouts()[name]
+    with pytest.raises(mk.MkError) as e:      # -1 is a CPU tensor's device number
+        mk._rows("call", "q", t, t.dtype, -1, (1, 8, 64))
+    assert e.value.status == mk.MK_ERR_INVALID
+    assert mk._row_stride(t) < 0              # the rule itself, which the compiled way asks too
+
+
+def test_layouts_that_are_taken():
+    import torch
+    x = torch.zeros(5, 12, 64)
+    rows = lambda t: mk._rows("call", "q", t, t.dtype, -1, tuple(t.shape))
+    assert rows(x) == 12 * 64 and rows(x[:, 2:6]) == 12 * 64 and rows(x[::2, :3]) == 2 * 12 * 64
+    # of one row the row stride does not matter, of one head the head stride, of none anything
+    assert rows(x[:1, 2:6]) == 4 * 64 and rows(x.as_strided((1, 12, 64), (7, 64, 1))) == 12 * 64
+    assert rows(x[:, ::12]) == 12 * 64 and rows(x[:0].transpose(1, 2)) == 12 * 64

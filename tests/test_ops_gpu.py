@@ -1159,3 +1159,70 @@ def test_decode_loop_in_one_graph(mk):
 
     for a, b in zip(loop(False), loop(True)):
         assert torch.equal(a, b)
+
+
+# ---- single rows: their heads and elements are contiguous too ------------------------------
+
+class FastNever:
+    """Stands for the compiled way: nothing is taken."""
+
+    def __getattr__(self, name):
+        return lambda *a: -1
+
+
+@pytest.mark.parametrize("fast", [True, False], ids=["compiled", "ctypes"])
+@pytest.mark.parametrize("layout", ["interleaved", "transposed", "sliced", "expanded heads", "expanded elements"])
+def test_single_rows_of_other_layouts_are_refused(mk, monkeypatch, fast, layout):
+    if not fast:
+        monkeypatch.setattr(mk, "_fast", FastNever())
+    g = gen(40)
+    cache = make_cache(mk, g, [40], 2, 64, 16, torch.bfloat16)
+    ws = mk.paged_attention_workspace(cache, 4, 40)
+    ok = lambda h: torch.zeros(1, h, 64, device="cuda", dtype=torch.bfloat16)
+    z = lambda *shape: torch.zeros(*shape, device="cuda", dtype=torch.bfloat16)
+    bad = {"interleaved": lambda h: z(1, h, 3, 64)[:, :, 1], "transposed": lambda h: z(1, 64, h).transpose(1, 2),
+           "sliced": lambda h: z(1, h, 128)[..., :64], "expanded heads": lambda h: z(1, 1, 64).expand(1, h, 64),
+           "expanded elements": lambda h: z(1, h, 1).expand(1, h, 64)}[layout]
+    cu, start, lens = ints([0, 1]), ints([3]), ints([40])
+    before = cache.k.clone(), cache.v.clone()
+    calls = []
+    for name, heads in (("q", 4), ("k", 2), ("v", 2), ("q_out", 4), ("k_out", 2)):
+        a = dict(q=ok(4), k=ok(2), v=ok(2), q_out=ok(4), k_out=ok(2))
+        a[name] = bad(heads)
+        calls.append(lambda a=a: mk.kv_append(cache, a["q"], a["k"], a["v"], cu, start, 1e4, a["q_out"], a["k_out"]))
+    for name in ("q", "out"):
+        a = dict(q=ok(4), out=ok(4))
+        a[name] = bad(4)
+        calls.append(lambda a=a: mk.paged_attention(cache, a["q"], lens, 40, a["out"], ws))
+    for name, heads in (("q", 4), ("k", 2), ("v", 2), ("out", 4)):
+        a = dict(q=ok(4), k=ok(2), v=ok(2), out=ok(4))
+        a[name] = bad(heads)
+        calls.append(lambda a=a: mk.prompt_attention(a["q"], a["k"], a["v"], cu, 1, a["out"]))
+    for call in calls:
+        with pytest.raises(mk.MkError) as e:
+            call()
+        assert e.value.status == mk.MK_ERR_INVALID
+    torch.cuda.synchronize()
+    same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))
+    assert same(cache.k, before[0]) and same(cache.v, before[1])
+
+
+@pytest.mark.parametrize("fast", [True, False], ids=["compiled", "ctypes"])
+def test_single_rows_of_any_row_stride(mk, monkeypatch, fast):
+    # one token of a fused buffer, whose row stride means nothing
+    if not fast:
+        monkeypatch.setattr(mk, "_fast", FastNever())
+    g = gen(41)
+    cache = make_cache(mk, g, [40], 2, 64, 16, torch.bfloat16)
+    buf = torch.randn(1, 9, 64, generator=g, device="cuda").bfloat16()
+    q, k, v = buf[:, :4].as_strided((1, 4, 64), (7, 64, 1)), buf[:, 4:6], buf[:, 6:8]
+    q0, k0 = q.clone(), k.clone()
+    out, ko, o = torch.empty_like(q0), torch.empty_like(k0), torch.empty_like(q0)
+    mk.kv_append(cache, q, k, v, ints([0, 1]), ints([39]), 1e4, out, ko)
+    for x, got in ((q0, out), (k0, ko)):
+        ref, r = rotate64(x, torch.tensor([39], device="cuda"), 1e4)
+        assert ((got.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -21 * r + 1e-7).all()
+    mk.paged_attention(cache, q, ints([40]), 40, o, mk.paged_attention_workspace(cache, 4, 40))
+    paged_check(cache, q0, [40], o, 0.125)
+    mk.prompt_attention(q, k, v, ints([0, 1]), 1, o)
+    prompt_check(q0, k0, v.contiguous(), [1], o, 0.125)
