@@ -51,6 +51,20 @@ struct PromptArgs {
     float scale;
     int32_t *status;
 };
+// The guard's share of a tile of 128 values (rows of 64 elements, in the
+// 128-byte swizzle; for 128 dims two halves one after the other): the 16-byte
+// vector that a lane of guard warp `half` looks at in a step, d / 8 steps in
+// all.  A warp's vectors hold the columns [half d / 2, + d / 2) of every row.
+// (64 dims: half a row of eight rows a step, in an order in which eight lanes
+// touch every bank once.)
+__host__ __device__ constexpr int guard_vector(int d, int half, int step, int lane) {
+    return d == 128 ? half * 1024 + step * 32 + lane
+                    : (step * 8 + (lane >> 3) + (lane & 4)) * 8 + ((((lane >> 2) & 1) ^ half) << 2 | (lane & 3));
+}
+// row and first column of a vector
+__host__ __device__ constexpr int guard_row(int vec) { return vec / 8 % 128; }
+__host__ __device__ constexpr int guard_column(int vec) { return vec / 1024 * 64 + ((vec ^ guard_row(vec)) & 7) * 8; }
+
 cudaError_t prompt_launch(const PromptArgs &a, int device, int num_sms, cudaStream_t stream);
 
 struct SampleArgs {

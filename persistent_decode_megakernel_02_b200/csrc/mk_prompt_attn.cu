@@ -27,7 +27,8 @@
 // weight times a NaN or an infinity is not zero, so in the tiles that hold
 // keys some row must not see, values that are not finite are taken out of
 // shared memory and remembered per column with their first key; the epilogue
-// adds them to the rows that do see them.
+// adds them to the rows that do see them.  Each guard warp has half of the
+// columns to itself, so that the two never wait for one another.
 //
 // The code is kept small (loops over sequences, a tile's loads and the rare
 // paths are not unrolled): at 92 KB the SMs fetched most of every short item's
@@ -101,7 +102,7 @@ struct PromptTail {
     PromptItem item[2];
     uint32_t tmem;
     int abort;
-    int any[2];             // a value was taken out
+    int any[2][2];          // a value was taken out, by the guard warp of its column
     int first[2][3][128];   // per column: first key (of the sequence) with NaN, +inf, -inf
 };
 static_assert(sizeof(PromptTail) <= 4096, "tail of the shared memory");
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                 mbar_init(&t.guard_done[i], 2);
                 mbar_init(&t.item_full[i], 1);
                 mbar_init(&t.item_empty[i], 11);   // issuer, 2 guard and 8 softmax warps
-                t.any[i] = 0;
+                t.any[i][0] = t.any[i][1] = 0;
             }
             t.abort = 0;
             fence_mbar_init();
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
         }
     } else if (warp >= 10) {
         // ---- guard of the masked tiles
-        const int gt = tid - 10 * 32;
+        const int half = warp - 10;
         int F = 0, masked[2] = {0, 0};
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -407,11 +408,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
             if (!ok) break;
             const int J = t.item[slot].tiles, blk0 = t.item[slot].blk[0], len = t.item[slot].len;
             if (J == 0) break;
-            if (t.any[slot]) {       // what the item before last left here
-                for (int i = gt; i < 3 * 128; i += 64) (&t.first[slot][0][0])[i] = 0x7fffffff;
-                asm volatile("bar.sync 1, 64;" ::: "memory");
-                if (gt == 0) t.any[slot] = 0;
-                asm volatile("bar.sync 1, 64;" ::: "memory");
+            if (t.any[slot][half]) {       // what the item before last left here
+                __syncwarp();
+                for (int i = lane; i < D / 2; i += 32)
+                    for (int kind = 0; kind < 3; ++kind) t.first[slot][kind][half * (D / 2) + i] = 0x7fffffff;
+                if (lane == 0) t.any[slot][half] = 0;
+                __syncwarp();
             }
             for (int which = 0; which < J - blk0 && ok; ++which) {
                 // the issuer says when the tile is there: a wait on the tile's own
@@ -421,30 +423,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                      mbar_wait_warp(&t.full[f % L::kStages], (f / L::kStages) & 1, &t.abort);
                 if (!ok) break;
                 uint4 *tile = reinterpret_cast<uint4 *>(smem + L::kRing + f % L::kStages * L::kTileBytes);
+                constexpr int kSteps = L::kTileBytes / 16 / 64;
                 constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u, kOne = kBf16 ? 0x00800080u : 0x04000400u;
                 uint32_t bad = 0;
 #pragma unroll 4
-                for (int i = gt; i < L::kTileBytes / 16; i += 64) {
-                    const uint4 x = tile[i];
+                for (int step = 0; step < kSteps; ++step) {
+                    const uint4 x = tile[guard_vector(D, half, step, lane)];
                     bad |= ((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne);
                 }
                 if (bad & 0x80008000u) {
                     uint16_t *e = reinterpret_cast<uint16_t *>(tile);
 #pragma unroll 1
-                    for (int i = gt; i < L::kTileBytes / 16; i += 64)
+                    for (int step = 0; step < kSteps; ++step) {
+                        const int i = guard_vector(D, half, step, lane), r = guard_row(i);
 #pragma unroll 1
                         for (int c = 0; c < 8; ++c) {
                             const uint32_t w = e[i * 8 + c];
                             if ((w & kExp & 0xffffu) != (kExp & 0xffffu)) continue;
                             e[i * 8 + c] = 0;
-                            const int half = i / (kTile * 8), r = i / 8 % kTile;
-                            const int col = half * 64 + ((i ^ r) & 7) * 8 + c;
+                            const int col = guard_column(i) + c;
                             if (j * kTile + r < len) {
                                 const int kind = (w & ~kExp & 0x7fffu) ? 0 : w & 0x8000u ? 2 : 1;
                                 atomicMin(&t.first[slot][kind][col], j * kTile + r);
-                                t.any[slot] = 1;
+                                t.any[slot][half] = 1;
                             }
                         }
+                    }
                     fence_async_smem();
                 }
                 __syncwarp();
@@ -578,7 +582,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                 const int row_first = blk * kTile + (warp & 3) * 32;
                 uint16_t *dst = (uint16_t *)a.out + (long long)(t.item[slot].row0 + row_first) * a.out_stride +
                                 (long long)t.item[slot].head[u] * D;
-                const bool any = t.any[slot] != 0;
+                const bool any = (t.any[slot][0] | t.any[slot][1]) != 0;
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t x[32];

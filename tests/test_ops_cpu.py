@@ -193,3 +193,24 @@ def test_layouts_that_are_taken():
     # of one row the row stride does not matter, of one head the head stride, of none anything
     assert rows(x[:1, 2:6]) == 4 * 64 and rows(x.as_strided((1, 12, 64), (7, 64, 1))) == 12 * 64
     assert rows(x[:, ::12]) == 12 * 64 and rows(x[:0].transpose(1, 2)) == 12 * 64
+
+
+def test_the_prompt_guard_s_warps_share_no_column(tmp_path):
+    """Two warps take values that are not finite out of a tile and remember them per column; if a
+    column belonged to both, one could wait for the other for good."""
+    import os
+    import subprocess
+    here, exe = os.path.dirname(os.path.abspath(__file__)), str(tmp_path / "guard_check")
+    subprocess.check_call(["g++", "-O1", "-std=c++17", "-I/usr/local/cuda/include", os.path.join(here, "guard_check.cpp"), "-o", exe])
+    out = subprocess.run([exe], capture_output=True, text=True)
+    assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout
+
+
+def test_the_serving_operators_wait_at_no_barrier_a_warp_may_miss():
+    """Named barriers have no bound: none is left where a role may give up alone."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(mk.LIB_PATH), "csrc")
+    for name in ("mk_prompt_attn.cu", "mk_tc.cuh", "mk_ops.cuh"):
+        with open(os.path.join(csrc, name)) as f:
+            assert not re.search(r"\bbar(rier)?\.(cta\.)?(sync|red|arrive)", f.read()), name

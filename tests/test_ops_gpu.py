@@ -1226,3 +1226,64 @@ def test_single_rows_of_any_row_stride(mk, monkeypatch, fast):
     paged_check(cache, q0, [40], o, 0.125)
     mk.prompt_attention(q, k, v, ints([0, 1]), 1, o)
     prompt_check(q0, k0, v.contiguous(), [1], o, 0.125)
+
+
+# ---- prompt attention: values that are not finite, broken offsets --------------------------
+
+def seen_not_finite(v, lens, nq):
+    """What a row's output must hold where it sees values that are not finite: NaN for a NaN or
+    both infinities, else the infinity; 0 where all it sees is finite."""
+    G, at = nq // v.shape[1], 0
+    want = torch.zeros(v.shape[0], nq, v.shape[2], device="cuda")
+    for n in lens:
+        x = v[at:at + n]
+        any_of = lambda m: m.long().cumsum(0) > 0
+        nan, pos, neg = any_of(x.isnan()), any_of(x == INF), any_of(x == -INF)
+        w = torch.where(pos, torch.full_like(want[at:at + n, :v.shape[1]], INF), torch.where(neg, -INF, 0.0))
+        w = torch.where(nan | (pos & neg), NAN, w)
+        want[at:at + n] = w.repeat_interleave(G, 1)
+        at += n
+    return want
+
+
+def prompt_poison_case(mk, lens, nq, nkv, d, dtype, at, seed=0):
+    """`at`: (row, KV head, column, value).  Rows that see one hold exactly what the formula gives
+    (scores of N(0,1) inputs leave every weight far above zero); all others the clean run's bits."""
+    q, k, v = prompt_inputs(lens, nq, nkv, d, dtype, seed)
+    clean, out, status = torch.empty_like(q), torch.full_like(q, 7.0), ints([0])
+    mk.prompt_attention(q, k, v, ints(cu_of(lens)), max(lens), clean)
+    prompt_check(q, k, v, lens, clean, d ** -0.5)
+    for row, h, col, x in at:
+        v[row, h, col] = x
+    mk.prompt_attention(q, k, v, ints(cu_of(lens)), max(lens), out, status=status)
+    assert int(status) == 0
+    want = seen_not_finite(v, lens, nq)
+    assert torch.equal(out[want == 0], clean[want == 0])
+    got = out.float()
+    assert torch.equal(got[want.isinf()], want[want.isinf()]) and got[want.isnan()].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", DT.values(), ids=DT.keys())
+@pytest.mark.parametrize("nq,nkv,d", [(2, 1, 64), (3, 1, 64), (6, 2, 128), (7, 1, 128), (4, 4, 64)])
+def test_prompt_values_that_are_not_finite(mk, dtype, nq, nkv, d):
+    # every column half and swizzle place, the last key of a tile, the first of the next, the very
+    # last, NaN and infinities of both signs in one column and in different ones
+    lens = [100, 300, 0, 257, 128]
+    starts = cu_of(lens)
+    at = [(starts[s] + r, c % nkv, c % d, x) for s, r, c, x in
+          [(0, 0, 0, INF), (0, 40, 0, INF), (0, 41, 5, NAN), (0, 99, 63, -INF), (1, 40, 33, INF), (1, 60, 33, -INF), (1, 127, 7, INF),
+           (1, 128, 8, -INF), (1, 255, 31, NAN), (1, 256, 32, INF), (1, 299, 64, NAN), (1, 290, 100, -INF), (3, 256, 127, INF),
+           (3, 130, 95, -INF), (3, 200, 96, NAN), (4, 127, 17, INF), (4, 126, 17, INF)]]
+    prompt_poison_case(mk, lens, nq, nkv, d, dtype, at, seed=nq)
+
+
+@pytest.mark.parametrize("lens,nq,nkv,d", [([20] * 700, 2, 1, 64), ([150] * 500, 3, 1, 128), ([200, 10] * 200, 8, 2, 64)])
+def test_prompt_values_that_are_not_finite_stay_with_their_item(mk, lens, nq, nkv, d):
+    # a block takes several items one after another: what one left behind must not reach the next
+    starts, rng = cu_of(lens), np.random.default_rng(len(lens))
+    at = []
+    for s in [*range(0, 150), *range(200, len(lens), 7)]:
+        for _ in range(3):
+            at.append((starts[s] + int(rng.integers(lens[s])), int(rng.integers(nkv)), int(rng.integers(d)),
+                       [INF, -INF, NAN][int(rng.integers(3))]))
+    prompt_poison_case(mk, lens, nq, nkv, d, torch.bfloat16, at, seed=1)
