@@ -1287,3 +1287,21 @@ def test_prompt_values_that_are_not_finite_stay_with_their_item(mk, lens, nq, nk
             at.append((starts[s] + int(rng.integers(lens[s])), int(rng.integers(nkv)), int(rng.integers(d)),
                        [INF, -INF, NAN][int(rng.integers(3))]))
     prompt_poison_case(mk, lens, nq, nkv, d, torch.bfloat16, at, seed=1)
+
+
+@pytest.mark.parametrize("cu", [[0, 10, 5, 20], [0, 10, 400, 20], [-4, 10, 15, 20], [0, 10, 15, 50], [3, 10, 15, 20]])
+def test_prompt_rows_of_broken_offsets(mk, cu):
+    # sequences that are whole are right, rows no such sequence claims stay
+    n, top = 30, 16
+    q, k, v = prompt_inputs([n], 2, 1, 64, torch.bfloat16)
+    out = torch.full_like(q, 7.0)
+    mk.prompt_attention(q, k, v, ints(cu), top, out)
+    claims = [[] for _ in range(n)]
+    for a, b in zip(cu, cu[1:]):
+        if 0 <= a <= b <= n and b - a <= top:
+            ref, mass = prompt_reference(q[a:b], k[a:b], v[a:b], [b - a], 0.125)
+            tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -11) * mass + 1e-7
+            for i, ok in enumerate((out[a:b].double() - ref).abs() <= tol):
+                claims[a + i].append(ok)
+    for i, c in enumerate(claims):        # of two claims each element has either's value
+        assert torch.stack(c).any(0).all() if c else (out[i] == 7).all(), i
