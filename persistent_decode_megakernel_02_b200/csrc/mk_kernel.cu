@@ -2447,9 +2447,8 @@ size_t tmem_pages_bytes(long long page_rows) { return (size_t)((page_rows + 15) 
 cudaError_t repack_tmem_pages(void *dst, const void *src, long long page_rows, cudaStream_t stream) {
     const long long total = (long long)(tmem_pages_bytes(page_rows) / 16);
     const long long blocks = (total + 255) / 256;
-    repack_tmem_pages_kernel<<<(unsigned)(blocks < 8192 ? blocks : 8192), 256, 0, stream>>>(
-        static_cast<uint4 *>(dst), static_cast<const uint4 *>(src), page_rows, total);
-    return cudaGetLastError();
+    return launch_kernel(repack_tmem_pages_kernel, (unsigned)(blocks < 8192 ? blocks : 8192), 256, 0, stream,
+                         static_cast<uint4 *>(dst), static_cast<const uint4 *>(src), page_rows, total);
 }
 
 cudaError_t kernel_launch(const Params &p, int grid, cudaStream_t stream) {

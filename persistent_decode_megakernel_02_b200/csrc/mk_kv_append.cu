@@ -95,13 +95,13 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(const __grid_constant__ A
 }
 
 template <class T, int D>
-void go(const AppendParams &p, int num_sms, cudaStream_t stream) {
+cudaError_t go(const AppendParams &p, int num_sms, cudaStream_t stream) {
     // More threads a token while there are SMs to spare (32/8/128 heads, 256
     // and 128 threads: 16 tokens 3.4 and 3.7 us, 256 4.3 and 4.5, 512 5.2 and
     // 5.1, 8192 41.8 and 37.3; two tokens a block: 38.4, four: 40.9)
     const int n = p.a.n_tokens;
-    if (n <= 2 * num_sms) kv_append_kernel<T, D, 256><<<n, 256, 0, stream>>>(p);
-    else kv_append_kernel<T, D, 128><<<n, 128, 0, stream>>>(p);
+    return n <= 2 * num_sms ? launch_kernel(kv_append_kernel<T, D, 256>, n, 256, 0, stream, p)
+                            : launch_kernel(kv_append_kernel<T, D, 128>, n, 128, 0, stream, p);
 }
 
 }  // namespace
@@ -115,14 +115,9 @@ cudaError_t append_launch(const AppendArgs &a, int num_sms, cudaStream_t stream)
     const double step = pow((double)a.theta, -1.0 / half);
     double f = 1.0 / 6.283185307179586476925286766559;
     for (int i = 0; i < half; ++i, f *= step) p.turn[i] = f;
-    if (a.kv.dtype == MK_BF16) {
-        if (a.kv.head_dim == 64) go<Bf16, 64>(p, num_sms, stream);
-        else go<Bf16, 128>(p, num_sms, stream);
-    } else {
-        if (a.kv.head_dim == 64) go<Fp16, 64>(p, num_sms, stream);
-        else go<Fp16, 128>(p, num_sms, stream);
-    }
-    return cudaGetLastError();
+    if (a.kv.dtype == MK_BF16)
+        return a.kv.head_dim == 64 ? go<Bf16, 64>(p, num_sms, stream) : go<Bf16, 128>(p, num_sms, stream);
+    return a.kv.head_dim == 64 ? go<Fp16, 64>(p, num_sms, stream) : go<Fp16, 128>(p, num_sms, stream);
 }
 
 }  // namespace mk

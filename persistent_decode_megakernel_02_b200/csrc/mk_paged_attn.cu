@@ -459,21 +459,16 @@ size_t paged_workspace(const mk_paged_kv &kv, int max_len, int, int num_sms) {
 }
 
 template <class T, int D>
-static void paged_go(const PagedParams &p, int grid, cudaStream_t stream) {
-    paged_attn_kernel<T, D><<<grid, PagedShape<D>::kThreads, 0, stream>>>(p);
+static cudaError_t paged_go(const PagedParams &p, int grid, cudaStream_t stream) {
+    return launch_kernel(paged_attn_kernel<T, D>, grid, PagedShape<D>::kThreads, 0, stream, p);
 }
 
 cudaError_t paged_launch(const PagedArgs &a, int, int num_sms, cudaStream_t stream) {
     PagedParams p{a, max_blocks(num_sms)};
     const int grid = grid_of(a.kv, a.max_len, num_sms);
-    if (a.kv.dtype == MK_BF16) {
-        if (a.kv.head_dim == 64) paged_go<Bf16, 64>(p, grid, stream);
-        else paged_go<Bf16, 128>(p, grid, stream);
-    } else {
-        if (a.kv.head_dim == 64) paged_go<Fp16, 64>(p, grid, stream);
-        else paged_go<Fp16, 128>(p, grid, stream);
-    }
-    return cudaGetLastError();
+    if (a.kv.dtype == MK_BF16)
+        return a.kv.head_dim == 64 ? paged_go<Bf16, 64>(p, grid, stream) : paged_go<Bf16, 128>(p, grid, stream);
+    return a.kv.head_dim == 64 ? paged_go<Fp16, 64>(p, grid, stream) : paged_go<Fp16, 128>(p, grid, stream);
 }
 
 }  // namespace mk

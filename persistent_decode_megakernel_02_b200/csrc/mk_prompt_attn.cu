@@ -687,8 +687,7 @@ cudaError_t launch(const PromptParams &p, int device, int grid, cudaStream_t str
         if (at.numRegs != kLaunchRegsPrompt) return cudaErrorInvalidDeviceFunction;
         ready[device].store(true, std::memory_order_relaxed);
     }
-    prompt_attn_kernel<T, D><<<grid, kPromptThreads, PromptSmem<D>::kBytes, stream>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(prompt_attn_kernel<T, D>, grid, kPromptThreads, PromptSmem<D>::kBytes, stream, p);
 }
 
 }  // namespace

@@ -12,6 +12,20 @@
 
 namespace mk {
 
+// Launch a kernel and return that launch's own status.  (After <<<>>> only
+// cudaGetLastError tells, and that also gives an error an earlier call of the
+// thread left behind: the launch would look refused although it runs.)
+template <class T>
+struct as_declared {
+    typedef T type;
+};
+template <class... P>
+cudaError_t launch_kernel(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                          typename as_declared<P>::type... args) {
+    void *a[] = {(void *)&args...};
+    return cudaLaunchKernel((const void *)kernel, dim3(grid), dim3(block), a, smem, stream);
+}
+
 // ---------------------------------------------------------------------------
 // PTX helpers
 // ---------------------------------------------------------------------------

@@ -1299,9 +1299,8 @@ cudaError_t repack_rows(uint16_t *dst, const uint16_t *src, const uint16_t *src2
                         cudaStream_t stream) {
     const long long total = (long long)tiles * (K / kRSlab) * kRTile * kRSlab;
     const long long blocks = (total + 255) / 256;
-    repack_rows_kernel<<<(unsigned)(blocks < 16384 ? blocks : 16384), 256, 0, stream>>>(dst, src, src2, rows, K,
-                                                                                        tiles);
-    return cudaGetLastError();
+    return launch_kernel(repack_rows_kernel, (unsigned)(blocks < 16384 ? blocks : 16384), 256, 0, stream, dst, src,
+                         src2, rows, K, tiles);
 }
 
 }  // namespace mk

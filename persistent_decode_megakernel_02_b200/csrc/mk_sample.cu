@@ -1050,10 +1050,7 @@ cudaError_t sample_launch(const SampleArgs &a, int device, int num_sms, cudaStre
     while (cluster < kMaxCluster && steps_of(cluster) > 1) cluster *= 2;
     while (cluster > 1 && (long long)a.rows * cluster > 2 * num_sms && steps_of(cluster / 2) <= kStepsForTwo) cluster /= 2;
     const int steps = steps_of(cluster);
-    if (steps > kMaxIt) {
-        sample_long_kernel<<<a.rows, kSampThreads, 0, stream>>>(a);
-        return cudaGetLastError();
-    }
+    if (steps > kMaxIt) return launch_kernel(sample_long_kernel, a.rows, kSampThreads, 0, stream, a);
     static std::atomic<bool> ready[kOpsMaxDevices];
     if (!ready[device].load(std::memory_order_relaxed)) {
         const cudaError_t e = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

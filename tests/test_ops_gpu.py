@@ -1305,3 +1305,61 @@ def test_prompt_rows_of_broken_offsets(mk, cu):
                 claims[a + i].append(ok)
     for i, c in enumerate(claims):        # of two claims each element has either's value
         assert torch.stack(c).any(0).all() if c else (out[i] == 7).all(), i
+
+
+# ---- an error that an earlier call left behind ----------------------------------------------
+
+def failed_create(mk):
+    """A context whose head alone is larger than any device: mk_create returns MK_ERR_OOM."""
+    from types import SimpleNamespace
+    shape = wl.ModelShape(name="huge head", layers=1, hidden=2048, n_q_heads=4, n_kv_heads=4, head_dim=64, ffn=64, tied=False,
+                          vocab=1 << 26, rope_theta=1e4, rms_eps=1e-5)
+    x = torch.zeros(1 << 20, device="cuda", dtype=torch.bfloat16)
+    w = SimpleNamespace(shape=shape, embed=x, lm_head=x, final_norm=x, **{n: [x] for n in (
+        "attn_norm", "mlp_norm", "wq", "wk", "wv", "wo", "wg", "wu", "wd")})
+    with pytest.raises(mk.MkError) as e:
+        mk.Context(w, [x], [x], 16, 1)
+    assert e.value.status == mk.MK_ERR_OOM
+
+
+def test_a_failed_create_does_not_reach_the_next_calls(mk):
+    # the failed allocation's error stays with the thread; a launch that went well must not be
+    # reported (and made again: rows rotated in place would turn twice)
+    g = gen(42)
+    for form in range(5):
+        cache = make_cache(mk, g, [40], 2, 64, 16, torch.bfloat16)
+        q, k, v = (torch.randn(20, h, 64, generator=g, device="cuda").bfloat16() for h in (4, 2, 2))
+        q0, k0 = q.clone(), k.clone()
+        ws = mk.paged_attention_workspace(cache, 4, 40)
+        out, o1, cu = torch.empty_like(q), torch.empty_like(q[:1]), ints([0, 20])
+        x, token = noise(2, 999, 40), ints([-7, -7])
+        xl, u = (noise(1, mk.MAX_VOCAB, 41) if form == 4 else None), torch.rand(2, device="cuda")
+        torch.cuda.synchronize()
+        failed_create(mk)
+        if form == 0:
+            mk.kv_append(cache, q, k, v, cu, ints([3]), 1e4, k_out=k)
+            for a, got in ((q0, q), (k0, k)):
+                ref, r = rotate64(a, torch.arange(3, 23, device="cuda"), 1e4)
+                assert ((got.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -21 * r + 1e-7).all()
+        elif form == 1:
+            mk.prompt_attention(q, k, v, cu, 20, out)
+            prompt_check(q, k, v, [20], out, 0.125)
+        elif form == 2:
+            mk.paged_attention(cache, q[:1], ints([40]), 40, o1, ws)
+            paged_check(cache, q[:1], [40], o1, 0.125)
+        elif form == 3:
+            mk.sample(x, u, token)
+            assert (token >= 0).all()
+        else:
+            mk.sample(xl, u[:1], token[:1])
+            assert token[0] >= 0
+    # and through the library's own functions, which say MK_OK
+    failed_create(mk)
+    lens, o1 = ints([40]), torch.empty_like(q[:1])
+    assert mk._lib.mk_paged_attention(cache._ref, lens.data_ptr(), 40, 4, q.data_ptr(), 256, 0.125, o1.data_ptr(), 256,
+                                      ws.data_ptr(), ws.numel(), None, torch.cuda.current_stream().cuda_stream) == mk.MK_OK
+    # a context that fits is made after one that did not
+    failed_create(mk)
+    w = wl.make_weights(wl.TINY, seed=5, device="cuda")
+    kc, vc = wl.make_kv(wl.TINY, 2, 48, device="cuda")
+    mk.Context(w, kc, vc, 48, 2).close()
