@@ -598,8 +598,10 @@ int mk_kv_append(const mk_paged_kv *kv, const int32_t *cu_tokens, const int32_t 
  *             before its first use; every call leaves it ready for the next
  *             one, of these or other sizes.  Calls (or graph replays) that may
  *             overlap on the device need one each.
- * Softmax statistics and sums are 32-bit.  Bad values: a length outside
- * [0, max_len] is clamped to it; positions on a page outside [0, num_pages)
+ * Softmax statistics and sums are 32-bit; a weight enters the value product
+ * to 2^-16 of itself (bf16), or to 2^-22 of itself or 2^-40 of the largest,
+ * whichever is more (fp16).  Bad values: a length outside [0, max_len] is
+ * clamped to it; positions on a page outside [0, num_pages)
  * are left out of the sums.
  */
 int mk_paged_attention(const mk_paged_kv *kv, const int32_t *kv_lens, int max_len, int n_q_heads, const void *q,

@@ -23,8 +23,11 @@
 // tensor rate either way.
 //
 // The softmax weights enter the value product as a 16-bit value and the
-// 16-bit remainder, in two products, so the output keeps the accuracy of
-// 32-bit weights.
+// 16-bit remainder, in two products.  In bf16 the two hold a weight to 2^-16 of
+// itself.  In fp16 they hold it to 2^-22, but nothing below 2^-25: so the
+// weights are scaled to at most 2^15 there, and what is lost of one is at most
+// 2^-40 of a warp's largest (with the largest at 1 to 2^8, as in bf16, 8192 keys
+// at 2^-20 of the largest were off by 3 % and vanished below 2^-25).
 //
 // What bounds it: 203000 positions in 32 sequences of 8 x 128 take 129 us,
 // 6.45 TB/s, 98 % of the copy rate.  At 34 MB (16 sequences of up to 2048, one
@@ -74,6 +77,16 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
+// A warp's reference maximum is raised when a score exceeds it by more than
+// kHead powers of two, and a weight is 2^(score - reference + kScale).  (In fp16
+// every rise raises it, or two powers of headroom and a scale of 2^13: 147 and
+// 147 us for 32 ragged sequences of up to 16384, 8 x 128, 12.5 and 12.5 for 16 of
+// up to 2048, 8 x 64.)
+template <class T>
+struct PagedWeight {
+    static constexpr float kHead = T::kBf16 ? 8.f : 0.f, kScale = T::kBf16 ? 0.f : 15.f;
+};
+
 template <int D>
 struct PagedShape {
     static constexpr int kGran = D == 64 ? 2 : 1;    // 16-key groups per step
@@ -99,6 +112,7 @@ struct PagedParams {
 template <class T, int D>
 __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(const __grid_constant__ PagedParams p) {
     using S = PagedShape<D>;
+    using W = PagedWeight<T>;
     constexpr int NW = S::kWarps, NT = S::kThreads, KG = S::kGran, JK = D / 32, JV = D / 64;
     __shared__ float so[NW][MK_MAX_GROUP][D];
     __shared__ float sm[NW][MK_MAX_GROUP], sl[NW][MK_MAX_GROUP];
@@ -275,8 +289,7 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
 #pragma unroll
             for (int k = 0; k < 2; ++k)
                 for (int o = 4; o < 32; o <<= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
-            // raise the reference maxima only when one rises by more than 2^8
-            const bool up = top[0] > m[0] + 8.f || top[1] > m[1] + 8.f;
+            const bool up = top[0] > m[0] + W::kHead || top[1] > m[1] + W::kHead;
             if (__any_sync(0xffffffffu, up)) {
                 float f[2];
 #pragma unroll
@@ -297,7 +310,7 @@ __global__ void __launch_bounds__(PagedShape<D>::kThreads, 2) paged_attn_kernel(
                 uint32_t hi2[2], lo2[2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const float w0 = ex2(s[r][2 * x] - m0), w1 = ex2(s[r][2 * x + 1] - m1);
+                    const float w0 = ex2(s[r][2 * x] - m0 + W::kScale), w1 = ex2(s[r][2 * x + 1] - m1 + W::kScale);
                     l[0] += w0;
                     l[1] += w1;
                     const uint32_t wh = T::pack(w0, w1);

@@ -1363,3 +1363,42 @@ def test_a_failed_create_does_not_reach_the_next_calls(mk):
     w = wl.make_weights(wl.TINY, seed=5, device="cuda")
     kc, vc = wl.make_kv(wl.TINY, 2, 48, device="cuda")
     mk.Context(w, kc, vc, 48, 2).close()
+
+
+# ---- many small weights beside a large one ---------------------------------------------------
+
+def spiked_scores(n, d, dtype, heads_at, far):
+    """Keys whose scores, in powers of two with scale = ln 2, are `far` at `heads_at` and 0 elsewhere;
+    values 0 there and of both signs elsewhere, so that the small weights make the result."""
+    k = torch.zeros(n, 1, d, device="cuda", dtype=dtype)
+    k[heads_at, 0, 0] = far
+    v = torch.ones(n, 1, d, device="cuda", dtype=dtype)
+    v[:, 0, 1::2] = -0.75
+    v[heads_at] = 0
+    return k, v
+
+
+@pytest.mark.parametrize("dtype", DT.values(), ids=DT.keys())
+@pytest.mark.parametrize("far", [12.25, 16.75, 19.625, 20.375, 22.625, 24.625, 25.5, 27.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_small_weights_are_kept(mk, dtype, far, d):
+    # 400 sequences over the same pages: a block has whole sequences, its warps every 8th (64 dims)
+    # or 6th step, and one large key each.  The tolerance is paged_check's, whose |v| has no share
+    # of the large keys.
+    n, page, seqs = 8192, 64, 400
+    step, warps = (32, 8) if d == 64 else (16, 6)
+    k, v = spiked_scores(n, d, dtype, [step * w + 3 for w in range(warps)], far)
+    pages = lambda x: x.view(n // page, page, 1, d).transpose(1, 2).contiguous()
+    cache = mk.PagedKV(pages(k), pages(v), torch.arange(n // page, device="cuda", dtype=torch.int32).repeat(seqs, 1))
+    q = torch.zeros(seqs, 2, d, device="cuda", dtype=dtype)
+    q[:, :, 0] = 1
+    out = torch.empty_like(q)
+    mk.paged_attention(cache, q, ints([n] * seqs), n, out, scale=math.log(2))
+    ref, mass = paged_reference(cache, q[:1], [n], math.log(2))
+    e = torch.finfo(dtype).eps
+    assert ((out.double() - ref).abs() <= e / 2 * ref.abs() + 2.0 ** -11 * mass + 1e-7).all(), (out[0, 0, :2], ref[0, 0, :2])
+    # and the large keys spread so that a warp meets one after many small ones
+    k, v = spiked_scores(n, d, dtype, [n - 1 - step * w for w in range(warps)], far)
+    cache.k.copy_(pages(k)), cache.v.copy_(pages(v))
+    mk.paged_attention(cache, q, ints([n] * seqs), n, out, scale=math.log(2))
+    assert ((out.double() - ref).abs() <= e / 2 * ref.abs() + 2.0 ** -11 * mass + 1e-7).all(), (out[0, 0, :2], ref[0, 0, :2])
