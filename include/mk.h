@@ -600,9 +600,10 @@ int mk_kv_append(const mk_paged_kv *kv, const int32_t *cu_tokens, const int32_t 
  *             overlap on the device need one each.
  * Softmax statistics and sums are 32-bit; a weight enters the value product
  * to 2^-16 of itself (bf16), or to 2^-22 of itself or 2^-40 of the largest,
- * whichever is more (fp16).  Bad values: a length outside [0, max_len] is
- * clamped to it; positions on a page outside [0, num_pages)
- * are left out of the sums.
+ * whichever is more (fp16).  An infinite value that a row sees makes its
+ * column infinite (NaN beside the other infinity or a NaN, and where its weight
+ * underflows).  Bad values: a length outside [0, max_len] is clamped to it;
+ * positions on a page outside [0, num_pages) are left out of the sums.
  */
 int mk_paged_attention(const mk_paged_kv *kv, const int32_t *kv_lens, int max_len, int n_q_heads, const void *q,
                        long long q_stride, float scale, void *out, long long out_stride, void *workspace,

@@ -1402,3 +1402,54 @@ def test_paged_small_weights_are_kept(mk, dtype, far, d):
     cache.k.copy_(pages(k)), cache.v.copy_(pages(v))
     mk.paged_attention(cache, q, ints([n] * seqs), n, out, scale=math.log(2))
     assert ((out.double() - ref).abs() <= e / 2 * ref.abs() + 2.0 ** -11 * mass + 1e-7).all(), (out[0, 0, :2], ref[0, 0, :2])
+
+
+# ---- paged attention: visible values that are not finite -------------------------------------
+
+@pytest.mark.parametrize("dtype", DT.values(), ids=DT.keys())
+@pytest.mark.parametrize("nq,nkv,d,page", [(8, 2, 64, 16), (8, 1, 128, 7), (3, 3, 64, 64), (4, 2, 128, 16)])
+def test_paged_values_that_are_not_finite(mk, dtype, nq, nkv, d, page):
+    # a column that sees an infinity holds it, one with a NaN or both signs NaN, every other the
+    # clean run's bits (the scores leave every weight far above zero)
+    lens = [1, 700, 40, 5000, 0, 33, 64]
+    g = gen(50 + d)
+    cache = make_cache(mk, g, lens, nkv, d, page, dtype)
+    q = torch.randn(len(lens), nq, d, generator=g, device="cuda").to(dtype)
+    clean, out = torch.empty_like(q), torch.full_like(q, 7.0)
+    mk.paged_attention(cache, q, ints(lens), max(lens), clean)
+    paged_check(cache, q, lens, clean, d ** -0.5)
+    want = torch.zeros(len(lens), nkv, d, device="cuda")
+    table = cache.page_table.tolist()
+    at = [(0, 0, 0, INF), (1, 0, 3, -INF), (1, 699, 4, INF), (1, 350, 5, NAN), (1, 17, 6, INF), (1, 500, 6, -INF), (1, 699, 63, -INF),
+          (2, 39, 31, INF), (3, 0, 1, INF), (3, 4999, 2, -INF), (3, 2500, 62, INF), (3, 2501, 62, INF), (3, 16, d - 1, NAN), (5, 32, d // 2, -INF),
+          (6, 63, 8, INF)]
+    for s, p, c, x in at:
+        h = c % nkv
+        cache.v[table[s][p // page], h, p % page, c] = x
+        w = want[s, h, c]
+        want[s, h, c] = x if w == 0 or w == x else NAN
+    mk.paged_attention(cache, q, ints(lens), max(lens), out)
+    want = want.repeat_interleave(nq // nkv, 1)
+    got = out.float()
+    assert torch.equal(got[want.isinf()], want[want.isinf()]) and got[want.isnan()].isnan().all()
+    assert torch.equal(out[want == 0], clean[want == 0])
+
+
+@pytest.mark.parametrize("far", [35.0, 42.0, 60.0])
+def test_paged_infinite_values_under_sharp_scores(mk, far):
+    # weights of one and of next to nothing (2^-far) times an infinity, and finite columns beside
+    # them as without it
+    n, d, page = 600, 64, 16
+    for dtype in DT.values():
+        k, v = spiked_scores(n, d, dtype, [5], far)
+        pages = lambda x: torch.cat([x, x[:608 - n]]).view(608 // page, page, 1, d).transpose(1, 2).contiguous()
+        cache = mk.PagedKV(pages(k), pages(v), torch.arange(608 // page, device="cuda", dtype=torch.int32)[None].contiguous())
+        q = torch.zeros(1, 2, d, device="cuda", dtype=dtype)
+        q[:, :, 0] = 1
+        clean, out = torch.empty_like(q), torch.empty_like(q)
+        mk.paged_attention(cache, q, ints([n]), n, clean, scale=math.log(2))
+        cache.v[0, 0, 5, 3], cache.v[0, 0, 6, 4], cache.v[0, 0, 5, 6], cache.v[20, 0, 1, 6] = INF, -INF, INF, -INF
+        mk.paged_attention(cache, q, ints([n]), n, out, scale=math.log(2))
+        assert (out[0, :, 3] == INF).all() and (out[0, :, 4] == -INF).all() and out[0, :, 6].isnan().all()
+        rest = [i for i in range(d) if i not in (3, 4, 6)]
+        assert torch.equal(out[..., rest], clean[..., rest])
