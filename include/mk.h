@@ -627,11 +627,14 @@ int mk_paged_attention_workspace(const mk_paged_kv *kv, int max_len, int n_q_hea
  *               [head_dim]; all of `dtype`.  out must not overlap q, k or v.
  * Values of later tokens or other sequences never reach a row, whatever they
  * hold (NaN and infinities included).  Scores, statistics and sums are
- * 32-bit; the softmax weights enter the value product in `dtype`.  Bad
- * values: a sequence whose rows are not 0 <= cu_seqlens[s] <=
- * cu_seqlens[s + 1] <= n_tokens or that is longer than max_len is left out
- * (its rows of out are not written; where cu_seqlens decreases, each element
- * of the rows that two sequences claim holds either's value).
+ * 32-bit; the softmax weights enter the value product in `dtype` (in fp16 to
+ * half a step of themselves down to 2^-25 of the row's largest, to 2^-36 of
+ * that below).  An infinite value that a row sees makes its column infinite,
+ * or NaN where its weight rounds to zero.  Bad values: a sequence whose rows
+ * are not 0 <= cu_seqlens[s] <= cu_seqlens[s + 1] <= n_tokens or that is longer
+ * than max_len is left out (its rows of out are not written; where cu_seqlens
+ * decreases, each element of the rows that two sequences claim holds either's
+ * value).
  */
 int mk_prompt_attention(int dtype, int n_q_heads, int n_kv_heads, int head_dim, const int32_t *cu_seqlens,
                         int n_seqs, int n_tokens, int max_len, const void *q, long long q_stride, const void *k,

@@ -17,9 +17,9 @@
 //   P = exp2(c S - c m)  (one thread per row; m a running reference maximum)
 //   O += P V_j           (P as 16-bit operand from tensor memory)
 // The reference m is raised, and O rescaled, only when a tile's maximum
-// exceeds it by more than 8 in the exponent of two: until then P stays
-// below 2^8, which costs no precision, and the rescaling pass over O is
-// rare.  l, the row's sum, stays in 32 bits in its thread; out = O / l.
+// exceeds it by more than 8 (fp16: 4) in the exponent of two: until then P stays
+// below a power of two that costs no precision, and the rescaling pass over O
+// is rare.  l, the row's sum, stays in 32 bits in its thread; out = O / l.
 //
 // Roles: warps 0-3 and 4-7 the softmax of unit 0 and 1 (warp w reads tensor
 // memory lanes 32 (w % 4)..), warp 8 the scheduler and TMA loader, warp 9 the
@@ -65,7 +65,17 @@ constexpr int kPromptThreads = 384;
 // registers would not end: prompt_launch refuses any other launch count.
 constexpr int kLaunchRegsPrompt = 168, kSoftmaxRegs = 208, kControlRegsPrompt = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kControlRegsPrompt == kPromptThreads * kLaunchRegsPrompt, "register split");
-constexpr float kRescale = 8.f;            // exponent headroom before O is rescaled
+// Exponent headroom before O is rescaled, and the scale of the weights, P =
+// 2^(score - reference + kScale).  fp16 has no exponents to spare: P goes up to
+// 2^15, so that a weight keeps its 11 bits down to 2^-25 of the row's largest and
+// is off by at most 2^-36 of it below.  (Headroom 8 / 4 / 2 / 0 in fp16: 8192 tokens
+// of 32/8/128 heads 463, 462, 498, 515 us with scores of N(0, 1), 477, 504, 510, 515
+// with three times their spread; unscaled 461 and 476, and weights of 2^-20 of the
+// largest off by 3 %, gone below 2^-25.)
+template <class T>
+struct PromptWeight {
+    static constexpr float kRescale = T::kBf16 ? 8.f : 4.f, kScale = T::kBf16 ? 0.f : 11.f;
+};
 
 // The larger of three (NaN is left out, as by fmaxf).
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -115,6 +125,7 @@ struct PromptParams {
 template <class T, int D>
 __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __grid_constant__ PromptParams p) {
     using L = PromptSmem<D>;
+    using W = PromptWeight<T>;
     constexpr bool kBf16 = T::kBf16;
     extern __shared__ __align__(1024) unsigned char smem[];
     PromptTail &t = *reinterpret_cast<PromptTail *>(smem + L::kTail);
@@ -510,7 +521,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                 for (int k = 0; k < 4; ++k) top4[k] = max3(top4[k], at(kTile - 4 + k), top4[k]);
                 const float top = max3(max3(top4[0], top4[1], top4[2]), top4[3], top4[3]);
                 const float old = m;
-                if (!((top - m) * c <= kRescale)) m = fmaxf(m, top);
+                if (!((top - m) * c <= W::kRescale)) m = fmaxf(m, top);
                 const bool raise = m != old;
                 // P and O are free once the tile before is weighted (128 dims: it is)
                 auto weighted = [&] {
@@ -536,7 +547,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_attn_kernel(const __
                         }
                 }
                 const float mc = m == -INFINITY ? 0.f : m * c;
-                const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+                const float2 c2 = make_float2(c, c), mc2 = make_float2(W::kScale - mc, W::kScale - mc);
                 float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
                 // (a share of the exponentials on the FMA units, by a polynomial,
                 // changed nothing between none and a quarter: 460, 459, 462 us at

@@ -1453,3 +1453,19 @@ def test_paged_infinite_values_under_sharp_scores(mk, far):
         assert (out[0, :, 3] == INF).all() and (out[0, :, 4] == -INF).all() and out[0, :, 6].isnan().all()
         rest = [i for i in range(d) if i not in (3, 4, 6)]
         assert torch.equal(out[..., rest], clean[..., rest])
+
+
+@pytest.mark.parametrize("dtype", DT.values(), ids=DT.keys())
+@pytest.mark.parametrize("far", [12.25, 16.75, 19.625, 20.375, 22.625, 24.625, 25.5])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_small_weights_are_kept(mk, dtype, far, d):
+    # one large key at the start of a long prompt (and, rows apart, in its middle) and small weights
+    # for all others, which make the result
+    n = 3000
+    for at in ([3], [1500, 1700]):
+        k, v = spiked_scores(n, d, dtype, at, far)
+        q = torch.zeros(n, 2, d, device="cuda", dtype=dtype)
+        q[:, :, 0] = 1
+        out = torch.empty_like(q)
+        mk.prompt_attention(q, k, v, ints([0, n]), n, out, scale=math.log(2))
+        prompt_check(q, k, v, [n], out, math.log(2))
