@@ -54,14 +54,43 @@ def _stale(lib: str = LIB, digest=None) -> bool:
         return f.read().strip() != (digest or _digest)()
 
 
+# Kernels that move registers between their warps: the shares add up to those of
+# a launch with exactly this many a thread (kLaunchRegs, kLaunchRegsPrompt), and
+# the library refuses to launch them with any other number.
+LAUNCH_REGISTERS = {"mk_step_kernel": 168, "prompt_attn_kernel": 168}
+
+
+def check_registers(log: str):
+    """Raise if `log`, what nvcc -Xptxas -v printed, shows another number of
+    registers for one of LAUNCH_REGISTERS, or none: the build would give a
+    library that refuses that kernel's calls."""
+    import re
+    seen = set()
+    for entry, n in re.findall(r"Compiling entry function '(\w+)'(?:(?!Compiling entry).)*?Used (\d+) registers", log, re.S):
+        for name, want in LAUNCH_REGISTERS.items():
+            if name in entry:
+                seen.add(name)
+                if int(n) != want:
+                    raise RuntimeError(f"{entry} was compiled to {n} registers a thread; its split needs {want}")
+    if missing := sorted(set(LAUNCH_REGISTERS) - seen):
+        raise RuntimeError(f"the compiler named no registers for {', '.join(missing)}")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if force or _stale():
         cmd = [_nvcc(), "-O3", "-std=c++17", *ARCH, "-t", "0", "-lineinfo", "-Xcompiler", "-fPIC", "-shared",
-               "-I", os.path.join(ROOT, "include"), "-o", LIB]
-        if verbose:
-            cmd += ["-Xptxas", "-v"]
+               "-I", os.path.join(ROOT, "include"), "-o", LIB, "-Xptxas", "-v"]
         cmd += [os.path.join(CSRC, f) for f in SOURCES]
-        subprocess.check_call(cmd)
+        done = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+        if verbose or done.returncode:
+            sys.stderr.write(done.stdout)
+        if done.returncode:
+            raise subprocess.CalledProcessError(done.returncode, cmd)
+        try:
+            check_registers(done.stdout)
+        except RuntimeError:
+            os.remove(LIB)
+            raise
         with open(STAMP, "w") as f:
             f.write(_digest())
     build_fast(force)

@@ -214,3 +214,33 @@ def test_the_serving_operators_wait_at_no_barrier_a_warp_may_miss():
     for name in ("mk_prompt_attn.cu", "mk_tc.cuh", "mk_ops.cuh"):
         with open(os.path.join(csrc, name)) as f:
             assert not re.search(r"\bbar(rier)?\.(cta\.)?(sync|red|arrive)", f.read()), name
+
+
+def compiler_log(**registers):
+    lines = []
+    for name, n in registers.items():
+        lines += [f"ptxas info    : Compiling entry function '_ZN2mk50_GLOBAL__N__92e1c366{name}INS_4Fp16ELi64EEEv' for 'sm_100a'",
+                  f"ptxas info    : Function properties for _ZN2mk50_GLOBAL__N__92e1c366{name}INS_4Fp16ELi64EEEv",
+                  "    8 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads", f"ptxas info    : Used {n} registers, used 1 barriers"]
+    return "\n".join(lines)
+
+
+def test_a_build_with_other_launch_registers_stops():
+    """Kernels that split their registers are refused at run time with any other number."""
+    from persistent_decode_megakernel_02_b200 import build as b
+    good = dict(mk_step_kernel=168, repack_rows_kernel=30, prompt_attn_kernel=168)
+    b.check_registers(compiler_log(**good))
+    for name in ("mk_step_kernel", "prompt_attn_kernel"):
+        with pytest.raises(RuntimeError, match=f"{name}.*160 registers"):
+            b.check_registers(compiler_log(**{**good, name: 160}))
+        with pytest.raises(RuntimeError, match=f"no registers for {name}"):
+            b.check_registers(compiler_log(**{k: v for k, v in good.items() if k != name}))
+
+
+def test_the_build_s_launch_registers_are_the_sources():
+    import os
+    import re
+    from persistent_decode_megakernel_02_b200 import build as b
+    text = "".join(open(os.path.join(b.CSRC, f)).read() for f in ("mk_internal.h", "mk_prompt_attn.cu"))
+    assert dict(re.findall(r"constexpr int (kLaunchRegs\w*) = (\d+)", text)) == {"kLaunchRegs": "168", "kLaunchRegsPrompt": "168"}
+    assert set(b.LAUNCH_REGISTERS.values()) == {168}
