@@ -97,6 +97,9 @@ int mk_kv_append(const mk_paged_kv *kv, const int32_t *cu_tokens, const int32_t 
     // an in-place output keeps its input's rows where they are
     if ((q_out == q && q && q_out_stride != q_stride) || (k_out == k && k_out_stride != k_stride)) return MK_ERR_INVALID;
     if (n_tokens == 0) return MK_OK;
+    // rows that overlap in any other way, as far as the first elements tell
+    if (q && (q_out == k || q_out == v || q_out == k_out || k_out == q)) return MK_ERR_INVALID;
+    if (k_out && k_out == v) return MK_ERR_INVALID;
     int dev, sms;
     const int st = ops_device(&dev, &sms);
     if (st != MK_OK) return st;
@@ -126,6 +129,7 @@ int mk_paged_attention(const mk_paged_kv *kv, const int32_t *kv_lens, int max_le
     const long long qw = (long long)n_q_heads * kv->head_dim;
     if (!rows_ok(q, q_stride, qw) || !rows_ok(out, out_stride, qw)) return MK_ERR_INVALID;
     if (!(scale > 0.f) || std::isinf(scale)) return MK_ERR_INVALID;
+    if (out == q && kv->n_seqs > 1 && out_stride != q_stride) return MK_ERR_INVALID;
     if (!aligned_or_null(workspace, 16)) return MK_ERR_INVALID;
     // the work, in steps of 16 positions and their overheads, fits an int
     if (((double)max_len / 16 + 32) * kv->n_seqs * kv->n_kv_heads > 2147000000.0) return MK_ERR_INVALID;
@@ -153,6 +157,7 @@ int mk_prompt_attention(int dtype, int n_q_heads, int n_kv_heads, int head_dim, 
         return MK_ERR_INVALID;
     if (!(scale > 0.f) || std::isinf(scale)) return MK_ERR_INVALID;
     if (n_tokens == 0) return MK_OK;
+    if (out == k || out == v) return MK_ERR_INVALID;      // read by other blocks meanwhile
     int dev, sms;
     const int st = ops_device(&dev, &sms);
     if (st != MK_OK) return st;

@@ -244,3 +244,26 @@ def test_the_build_s_launch_registers_are_the_sources():
     text = "".join(open(os.path.join(b.CSRC, f)).read() for f in ("mk_internal.h", "mk_prompt_attn.cu"))
     assert dict(re.findall(r"constexpr int (kLaunchRegs\w*) = (\d+)", text)) == {"kLaunchRegs": "168", "kLaunchRegsPrompt": "168"}
     assert set(b.LAUNCH_REGISTERS.values()) == {168}
+
+
+def test_outputs_over_inputs_that_are_still_read():
+    """Rows may be rotated in place; an output over another operand is refused, as far as the first
+    elements show it."""
+    own = dict(q=A, k=2 * A, v=3 * A, qo=4 * A, ko=5 * A, kos=128)
+    for bad in (dict(qo=2 * A), dict(qo=3 * A), dict(ko=3 * A), dict(ko=A), dict(ko=4 * A), dict(k=A, qo=A), dict(v=A, qo=A),
+                dict(v=2 * A, ko=2 * A)):
+        assert append(**{**own, **bad}) == mk.MK_ERR_INVALID, bad
+    for bad in (dict(out=2 * A), dict(out=3 * A)):
+        assert prompt(**{**dict(q=A, k=2 * A, v=3 * A, out=4 * A, os=256), **bad}) == mk.MK_ERR_INVALID, bad
+    assert paged(q=A, out=A, qs=256, os=512) == mk.MK_ERR_INVALID
+
+
+@pytest.mark.skipif(__import__("torch").cuda.is_available(), reason="made-up pointers")
+def test_the_forms_in_place_pass_the_checks():
+    # without a device the next thing a call meets is its absence
+    own = dict(q=A, k=2 * A, v=3 * A, qo=4 * A, ko=5 * A, kos=128)
+    for ok in (dict(), dict(qo=A), dict(ko=2 * A), dict(qo=A, ko=2 * A), dict(ko=None), dict(nq=0, q=None, qo=None),
+               dict(nq=0, q=None, qo=None, ko=2 * A)):
+        assert append(**{**own, **ok}) == mk.MK_ERR_CUDA, ok
+    assert prompt(q=A, k=2 * A, v=3 * A, out=4 * A) == mk.MK_ERR_CUDA
+    assert paged(q=A, out=A) == mk.MK_ERR_CUDA
