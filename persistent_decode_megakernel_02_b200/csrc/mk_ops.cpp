@@ -116,7 +116,7 @@ int mk_paged_attention_workspace(const mk_paged_kv *kv, int max_len, int n_q_hea
     int dev, sms;
     const int st = ops_device(&dev, &sms);
     if (st != MK_OK) return st;
-    *bytes_out = paged_workspace(*kv, max_len, n_q_heads, sms);
+    *bytes_out = paged_workspace(*kv, max_len, sms);
     return MK_OK;
 }
 
@@ -136,10 +136,10 @@ int mk_paged_attention(const mk_paged_kv *kv, const int32_t *kv_lens, int max_le
     int dev, sms;
     const int st = ops_device(&dev, &sms);
     if (st != MK_OK) return st;
-    const size_t need = paged_workspace(*kv, max_len, n_q_heads, sms);
+    const size_t need = paged_workspace(*kv, max_len, sms);
     if (!workspace || workspace_bytes < need) return MK_ERR_INVALID;
     PagedArgs a{*kv, kv_lens, max_len, n_q_heads, q, out, q_stride, out_stride, scale, workspace, status_out};
-    return launched(paged_launch(a, dev, sms, (cudaStream_t)stream));
+    return launched(paged_launch(a, sms, (cudaStream_t)stream));
 }
 
 int mk_prompt_attention(int dtype, int n_q_heads, int n_kv_heads, int head_dim, const int32_t *cu_seqlens,

@@ -38,8 +38,8 @@ struct PagedArgs {
     void *workspace;
     int32_t *status;
 };
-size_t paged_workspace(const mk_paged_kv &kv, int max_len, int n_q_heads, int num_sms);
-cudaError_t paged_launch(const PagedArgs &a, int device, int num_sms, cudaStream_t stream);
+size_t paged_workspace(const mk_paged_kv &kv, int max_len, int num_sms);
+cudaError_t paged_launch(const PagedArgs &a, int num_sms, cudaStream_t stream);
 
 struct PromptArgs {
     int dtype, nq, nkv, d;

@@ -510,7 +510,7 @@ static int grid_of(const mk_paged_kv &kv, int max_len, int num_sms) {
     return (int)(want < 1 ? 1 : want > max_blocks(num_sms) ? max_blocks(num_sms) : want);
 }
 
-size_t paged_workspace(const mk_paged_kv &kv, int max_len, int, int num_sms) {
+size_t paged_workspace(const mk_paged_kv &kv, int max_len, int num_sms) {
     return counter_bytes(max_blocks(num_sms)) +
            (size_t)grid_of(kv, max_len, num_sms) * 2 * slot_floats(kv.head_dim) * sizeof(float);
 }
@@ -520,7 +520,7 @@ static cudaError_t paged_go(const PagedParams &p, int grid, cudaStream_t stream)
     return launch_kernel(paged_attn_kernel<T, D>, grid, PagedShape<D>::kThreads, 0, stream, p);
 }
 
-cudaError_t paged_launch(const PagedArgs &a, int, int num_sms, cudaStream_t stream) {
+cudaError_t paged_launch(const PagedArgs &a, int num_sms, cudaStream_t stream) {
     PagedParams p{a, max_blocks(num_sms)};
     const int grid = grid_of(a.kv, a.max_len, num_sms);
     if (a.kv.dtype == MK_BF16)

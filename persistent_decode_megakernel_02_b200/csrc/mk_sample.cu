@@ -156,8 +156,8 @@ struct SampShared {
     uint32_t tmp32[kSampWarps];
     double table[32];
     uint32_t bin;
-    u64 mass_before, mass_bin;
-    uint32_t cnt_before, cnt_bin;
+    u64 mass_before;
+    uint32_t cnt_before;
 };
 
 __global__ void __launch_bounds__(kSampThreads) sample_long_kernel(SampleArgs a) {
@@ -243,7 +243,6 @@ __global__ void __launch_bounds__(kSampThreads) sample_long_kernel(SampleArgs a)
                 sh.bin = 2 * tid + (r1 ? 0 : 1);
                 sh.cnt_before = r1 ? cb : cb + c0;
                 sh.mass_before = r1 ? mb : mb + m0;
-                sh.cnt_bin = r1 ? c0 : c1;
             }
             __syncthreads();
             const uint32_t bin = sh.bin;
@@ -372,7 +371,6 @@ struct RegShared {
     uint32_t list_n;
     u64 tmp64[kRegWarps];
     uint32_t tmp32[kRegWarps];
-    u64 goal;
 };
 
 static_assert(sizeof(RegShared) + kMaxIt * kVecStep * 4 <= 227 * 1024, "a slice fits a block's shared memory");
@@ -671,8 +669,8 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
     int32_t last = 0x7fffffff;
 
     // The histogram bins of all blocks (filled, not yet synchronised): the
-    // first bin at which reached(count, mass, all mass) turns true over the
-    // running totals, with what lies before it, in sh.found_*.  False if none.
+    // first bin at which reached(count, mass) turns true over the running totals,
+    // with its count and what lies before it, in sh.found_*.  False if none.
     auto find_bin = [&](auto reached, bool masses, uint32_t cnt0, u64 mass0) {
         cl.sync();
         // every block adds up its share of the bins, consecutive ones per thread
@@ -706,7 +704,7 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
         }
         if (lane == 31) { sh.tmp32[warp] = cs; sh.tmp64[warp] = ms; }
         __syncthreads();
-        uint32_t ctot = 0, cb = cs - csum;
+        uint32_t ctot = 0, cb = cs - csum;      // of the block, and before this thread
         u64 mtot = 0, mb = ms - msum;
 #pragma unroll
         for (int w = 0; w < kRegWarps; ++w) {
@@ -722,21 +720,19 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
         cl.sync();
         cb += cnt0;
         mb += mass0;
-        u64 total = mass0;
-        for (int r = 0; r < CL; ++r) {
-            if (r < rank) { cb += sh.x_cnt[r]; mb += sh.x_mass[r]; }
-            total += sh.x_mass[r];
+        for (int r = 0; r < rank; ++r) {
+            cb += sh.x_cnt[r];
+            mb += sh.x_mass[r];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (i < per && tid * per + i < share && !reached(cb, mb, total) && reached(cb + c[i], mb + m[i], total)) {
+            if (i < per && tid * per + i < share && !reached(cb, mb) && reached(cb + c[i], mb + m[i])) {
                 for (int r = 0; r < CL; ++r) {
                     RegShared *o = cl.map_shared_rank(&sh, r);
                     o->found_bin = lo + tid * per + i;
                     o->found_before = cb;
                     o->found_cnt = c[i];
                     o->found_mass = mb;
-                    o->goal = total;
                 }
             }
             cb += c[i];
@@ -997,7 +993,7 @@ __global__ void __launch_bounds__(kRegThreads, 2) sample_kernel(SampleArgs a, in
                 if (by_mass) atomicAdd(&sh.mass[b], wt.whole(f));
             });
             if (!find_bin(
-                    [&](uint32_t c, u64 m, u64) { return by_mass ? c > 0 && (double)m >= target : c >= (uint32_t)k; },
+                    [&](uint32_t c, u64 m) { return by_mass ? c > 0 && (double)m >= target : c >= (uint32_t)k; },
                     by_mass, cnt_above, mass_above))
                 break;      // fewer than k: all stay
             cnt_above = sh.found_before;
