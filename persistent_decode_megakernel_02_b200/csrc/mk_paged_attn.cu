@@ -29,11 +29,11 @@
 // 2^-40 of a warp's largest (with the largest at 1 to 2^8, as in bf16, 8192 keys
 // at 2^-20 of the largest were off by 3 % and vanished below 2^-25).
 //
-// What bounds it: 203000 positions in 32 sequences of 8 x 128 take 129 us,
-// 6.45 TB/s, 98 % of the copy rate.  At 34 MB (16 sequences of up to 2048, one
-// of 16385: 13.7 and 12.6 us, 5.2 by the copy rate) the chain of dependent
+// What bounds it: 203000 positions in 32 sequences of 8 x 128 take 128 us,
+// 6.5 TB/s, 99 % of the copy rate.  At 34 MB (16 sequences of up to 2048, one
+// of 16385: 14.3 and 12.9 us, 5.2 by the copy rate) the chain of dependent
 // latencies around the stream does: lengths, page table, first rows, and the
-// merge through the workspace; one sequence of 551 is that chain alone, 6.7 us.
+// merge through the workspace; one sequence of 551 is that chain alone, 7.1 us.
 #include "mk_ops.cuh"
 
 namespace mk {

@@ -33,17 +33,20 @@
 // The code is kept small (loops over sequences, a tile's loads and the rare
 // paths are not unrolled): at 92 KB the SMs fetched most of every short item's
 // code from the instruction cache that a cluster of them shares, at 92 % of
-// its rate.  At 66 KB 1000 prompts of 20 tokens take 524 us instead of 559, 100
-// of 200 tokens 130 instead of 142; rolling the epilogue and the issuer's loop
+// its rate.  At 66 KB 1000 prompts of 20 tokens took 524 us instead of 559 (532
+// since the guard's warps have their own columns), 100 of 200 tokens 130 instead
+// of 142; rolling the epilogue and the issuer's loop
 // over the units too (53 KB) gives 469 and 135, but costs long prompts 5 %.
 //
 // What bounds it: a unit's tile is a chain (products, softmax, products; 1024
 // cycles of matrix work at 128 dims, and 1320 of a softmax warp alone, 1760
 // beside the other unit's), of which the two units overlap two: 8192 tokens
-// of 32/8/128 heads 447 us, 1.23 PFLOP/s, 76 % of the matrix peak measured in
-// bursts.  With 64 dims the products are half of that and the softmax is what
-// remains: 6811 tokens in 9 prompts 72 us.  Short prompts by the latency of
-// one tile's chain from load to store.
+// of 32/8/128 heads 442 us, 1.24 PFLOP/s, 77 % of the matrix peak measured in
+// bursts.  With 64 dims the products are half of that and the chain's latency
+// remains: 6811 tokens in 9 prompts 73 us, with the matrix unit 22 %, the unit of
+// the exponentials 51 % and the issue slots 37 % busy -- two units in flight and two
+// softmax warps a scheduler do not fill any of them.  Short prompts by the
+// latency of one tile's chain from load to store.
 //
 // Tensor memory, 512 columns: S0 | S1 | O0 | O1, and for 64 dims P0 | P1: the
 // next tile's S is then computed while this one's softmax runs.  For 128 dims

@@ -333,7 +333,9 @@ constexpr int kRegThreads = 512, kRegWarps = kRegThreads / 32, kMaxCluster = 8;
 constexpr int kListMax = 512;                  // gathered logits, at most
 // top-k by the threads' maxima, at most (one row of 128256, against the exact
 // cut: k = 50 10.3 and 32.3 us, 200 14.8 and 32.5, 384 24.6 and 32.8; 64 rows of
-// 32000: 10.8 and 32.8, 19.5 and 33.4, 39.5 and 33.8)
+// 32000: 10.8 and 32.8, 19.5 and 33.4, 39.5 and 33.8).  Chosen for few rows: with
+// 64 the two ways cross between 200 and 384, above which this one costs up to a
+// sixth more, as the pairwise ranking grows with k^2 in every row's first block.
 constexpr int kMaxK = 384;
 constexpr int kVecStep = 4 * kRegThreads;      // logits of one vector step of a block
 constexpr int kMaxIt = 22;                     // vector steps of a slice: 176 KB of logits
