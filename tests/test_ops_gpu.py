@@ -1469,3 +1469,34 @@ def test_prompt_small_weights_are_kept(mk, dtype, far, d):
         out = torch.empty_like(q)
         mk.prompt_attention(q, k, v, ints([0, n]), n, out, scale=math.log(2))
         prompt_check(q, k, v, [n], out, math.log(2))
+
+
+# exponents whose power of two lies near the middle of two 16-bit values
+DOWN = {"bf16": [0.9609375, 0.8046875, 0.578125], "fp16": [0.9921875, 0.9453125, 0.8046875]}
+
+
+@pytest.mark.parametrize("dtype,down", [(torch.bfloat16, x) for x in DOWN["bf16"]] + [(torch.float16, x) for x in DOWN["fp16"]], ids=str)
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_weights_keep_their_remainder(mk, dtype, down, d):
+    # Every 16th key scores 0 with value 0, all others -down (powers of two), so that each weight is
+    # off by the same share when it is rounded to 16 bits.  Beyond the output's rounding: the two
+    # parts hold a weight to 2^-16, ex2 to 2^-22, a score's 32-bit scaling to 2^-23, and 512 products
+    # added in 32 bits lose at most 512 * 2^-24 = 2^-15: below 2^-14 in all.
+    n, page = 4096, 64
+    g = gen(60)
+    k = torch.zeros(n, 1, d, device="cuda", dtype=dtype)
+    k[:, 0, 0] = -down
+    k[::16] = 0
+    v = (0.5 + torch.rand(1, 1, d, generator=g, device="cuda")).to(dtype).repeat(n, 1, 1)
+    v[::16] = 0
+    pages = lambda x: x.view(n // page, page, 1, d).transpose(1, 2).contiguous()
+    cache = mk.PagedKV(pages(k), pages(v), torch.arange(n // page, device="cuda", dtype=torch.int32)[None].contiguous())
+    q = torch.zeros(1, 3, d, device="cuda", dtype=dtype)
+    q[:, :, 0] = 1
+    out = torch.empty_like(q)
+    mk.paged_attention(cache, q, ints([n]), n, out, scale=math.log(2))
+    ref, mass = paged_reference(cache, q, [n], math.log(2))
+    fine = lambda x: ((x.double() - ref).abs() <= torch.finfo(dtype).eps / 2 * ref.abs() + 2.0 ** -14 * mass).all()
+    assert fine(out)
+    w = 2.0 ** -down         # and the check sees a weight that is rounded once
+    assert fine(ref.to(dtype)) and not fine((ref * (float(torch.tensor(w).to(dtype)) / w)).to(dtype))
