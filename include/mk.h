@@ -583,8 +583,8 @@ int mk_kv_append(const mk_paged_kv *kv, const int32_t *cu_tokens, const int32_t 
  * of sequence s, with h = i / (n_q_heads / n_kv_heads),
  *   out[s][i] = sum_j softmax_j(scale * q[s][i] . k[j][h]) v[j][h],
  *   j < kv_lens[s].
- * A sequence of length 0 gives zeros.  Positions from kv_lens[s] on are not
- * read.
+ * A sequence of length 0 gives zeros, and so does a head all of whose scores
+ * are -infinity.  Positions from kv_lens[s] on are not read.
  *   kv_lens   device int32 [n_seqs]
  *   max_len   host bound on kv_lens (at most pages_per_seq * page_size): it
  *             sizes the launch and the workspace, so that the same launch can
@@ -626,7 +626,8 @@ int mk_paged_attention_workspace(const mk_paged_kv *kv, int max_len, int n_q_hea
  *   q, out      [n_tokens][n_q_heads][head_dim]; k, v [n_tokens][n_kv_heads]
  *               [head_dim]; all of `dtype`.  out must not overlap q, k or v.
  * Values of later tokens or other sequences never reach a row, whatever they
- * hold (NaN and infinities included).  Scores, statistics and sums are
+ * hold (NaN and infinities included).  A head all of whose scores are -infinity
+ * gives zeros.  Scores, statistics and sums are
  * 32-bit; the softmax weights enter the value product in `dtype` (in fp16 to
  * half a step of themselves down to 2^-25 of the row's largest, to 2^-36 of
  * that below).  An infinite value that a row sees makes its column infinite,

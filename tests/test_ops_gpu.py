@@ -1500,3 +1500,25 @@ def test_paged_weights_keep_their_remainder(mk, dtype, down, d):
     assert fine(out)
     w = 2.0 ** -down         # and the check sees a weight that is rounded once
     assert fine(ref.to(dtype)) and not fine((ref * (float(torch.tensor(w).to(dtype)) / w)).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", DT.values(), ids=DT.keys())
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_minus_infinity_only(mk, dtype, d):
+    # zeros where nothing but such keys is seen, the formula where one finite score joins them
+    g = gen(61)
+    n, page = 200, 16
+    q = torch.ones(n, 2, d, device="cuda", dtype=dtype)
+    k, v = (torch.randn(n, 1, d, generator=g, device="cuda").to(dtype) for _ in range(2))
+    k[:150, :, 3] = -INF
+    out, status = torch.full_like(q, NAN), ints([0])
+    mk.prompt_attention(q, k, v, ints([0, n]), n, out, status=status)
+    assert (out[:150] == 0).all()
+    prompt_check(q[150:], k[150:], v[150:], [n - 150], out[150:], d ** -0.5)
+    pad = lambda x: torch.cat([x, x[:8]]).view(13, page, 1, d).transpose(1, 2).contiguous()
+    cache = mk.PagedKV(pad(k), pad(v), torch.arange(13, device="cuda", dtype=torch.int32).repeat(4, 1))
+    lens = [1, 150, 151, 200]
+    o = torch.full_like(q[:4], NAN)
+    mk.paged_attention(cache, q[:4].contiguous(), ints(lens), n, o, status=status)
+    assert (o[:2] == 0).all() and int(status) == 0
+    paged_check(cache, q[:4], lens, o, d ** -0.5, sel=[2, 3])
